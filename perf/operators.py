@@ -245,6 +245,13 @@ def _plain_project(st):
     return (st["x"].float() @ w.t()).to(DTYPE[c["dtype"]])
 
 
+def _nearest_fp8(x):
+    """The nearest e4m3 value of each, ties to even, rounded once from fp64 (a cast would go through fp32)."""
+    x = x.clamp(-FP8_MAX, FP8_MAX)
+    grid = (torch.frexp(x).exponent - 1).clamp_min(-6) - 3
+    return torch.ldexp(torch.round(torch.ldexp(x, -grid)), grid).to(FP8)
+
+
 def _plain_append(st):
     c = st["case"]
     s, n, h, d, p = c["seqs"], c["new"], c["kv_heads"], c["head_dim"], c["page"]
@@ -277,7 +284,7 @@ def _plain_append(st):
         kept = torch.where((scale > was)[:, :, None, None] & older[:, None, :, None],
                            old * (was / scale)[:, :, None, None], old)
         code = torch.where(fresh, dense / scale[:, :, None, None], kept)
-        st[name][ids] = code.clamp(-FP8_MAX, FP8_MAX).to(FP8)
+        st[name][ids] = _nearest_fp8(code)
         st[name + "_scale"][ids] = scale.float()
     return {x: st[x] for x in ("k", "v", "k_scale", "v_scale")}
 
