@@ -2,39 +2,66 @@
 package so that the library travels with the source tree.
 
 The library is rebuilt unless a stamp file beside it records the SHA-256 of
-every source it is built from and of the nvcc command: a binary that merely
-has a later modification time than its sources is not trusted."""
+every source it is built from and of the nvcc commands: a binary that merely
+has a later modification time than its sources is not trusted.  Each
+translation unit keeps an object with a stamp of its own."""
 
 import hashlib
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "mono_ffn.cu")
-DEPS = [SRC] + [os.path.join(PKG, "csrc", f) for f in ("common.cuh", "cc_kernel.cuh", "tc_kernel.cuh", "ptx.cuh",
-                                                         "route_noalloc.cuh", "tq_kernel.cuh")] + \
-       [os.path.join(ROOT, "include", "mono_ffn.h")]
+INCLUDE = os.path.join(ROOT, "include")
+# translation units and what each is built from
+UNITS = {
+    "mono_ffn": ["mono_ffn.cu", "common.cuh", "cc_kernel.cuh", "tc_kernel.cuh", "ptx.cuh", "route_noalloc.cuh",
+                 "tq_kernel.cuh", "mono_ffn.h"],
+    "mono_attn": ["mono_attn.cu", "proj.cuh", "kv_attend.cuh", "kv_append.cuh", "rope.cuh", "kv_index.h", "ptx.cuh",
+                  "mono_ffn.h", "mono_attn.h"],
+}
 SO = os.path.join(PKG, "libmonoffn.so")
 STAMP = SO + ".sha256"
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17", "-maxrregcount=168",
               "-Xcompiler", "-fPIC",
-              "-shared", "-Xptxas", "-v"]
+              "-Xptxas", "-v"]
+
+
+def _path(name):
+    return os.path.join(INCLUDE if name.endswith(".h") and name.startswith("mono_") else os.path.join(PKG, "csrc"), name)
+
+
+def _object(unit):
+    return os.path.join(PKG, unit + ".o")
+
+
+def compile_command(unit):
+    return ["nvcc", *NVCC_FLAGS, "-I", INCLUDE, "-c", "-o", _object(unit), _path(UNITS[unit][0])]
 
 
 def command():
-    return ["nvcc", *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", SO, SRC]
+    """The link step."""
+    return ["nvcc", "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", SO, *map(_object, UNITS)]
+
+
+def unit_hash(unit):
+    h = hashlib.sha256()
+    for d in UNITS[unit]:
+        h.update(d.encode() + b"\0")
+        with open(_path(d), "rb") as f:
+            h.update(f.read())
+    h.update(" ".join(compile_command(unit)).encode())
+    return h.hexdigest()
 
 
 def source_hash():
-    """SHA-256 over the sources (name and bytes, in a fixed order) and the
-    nvcc command line."""
+    """SHA-256 over every unit's sources (name and bytes, in a fixed order) and
+    the nvcc commands."""
     h = hashlib.sha256()
-    for d in DEPS:
-        h.update(os.path.basename(d).encode() + b"\0")
-        with open(d, "rb") as f:
-            h.update(f.read())
+    for u in UNITS:
+        h.update(unit_hash(u).encode())
     h.update(" ".join(command()).encode())
     return h.hexdigest()
 
@@ -46,18 +73,39 @@ def up_to_date():
         return f.read().strip() == source_hash()
 
 
+def _run(cmd):
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    log = " ".join(cmd) + "\n" + res.stdout + res.stderr
+    if res.returncode != 0:
+        raise RuntimeError("nvcc failed:\n" + log[-4000:])
+    return log
+
+
+def _compile(unit, force):
+    """One unit's object, unless the stamp beside it records these sources."""
+    stamp = _object(unit) + ".sha256"
+    if not force and os.path.exists(_object(unit)) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == unit_hash(unit):
+                return ""
+    if os.path.exists(stamp):
+        os.unlink(stamp)
+    log = _run(compile_command(unit))
+    with open(stamp, "w") as f:
+        f.write(unit_hash(unit) + "\n")
+    return log
+
+
 def build(force=False, verbose=False):
     if not force and up_to_date():
         return SO
     if os.path.exists(STAMP):
         os.unlink(STAMP)
-    cmd = command()
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    log = res.stdout + res.stderr
+    with ThreadPoolExecutor(len(UNITS)) as pool:   # nvcc runs in its own process
+        logs = list(pool.map(lambda u: _compile(u, force), UNITS))
+    log = "".join(logs) + _run(command())
     with open(os.path.join(PKG, "build.log"), "w") as f:
-        f.write(" ".join(cmd) + "\n" + log)
-    if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + log[-4000:])
+        f.write(log)
     with open(STAMP, "w") as f:
         f.write(source_hash() + "\n")
     if verbose:
