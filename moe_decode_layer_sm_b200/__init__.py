@@ -10,5 +10,6 @@ _ATTN = ("Rope", "rope", "KVCache", "AttnPlan", "Projection")
 def __getattr__(name):   # attn.py imports torch; binding.py does so only where it needs it
     if name in _ATTN:
         from . import attn
-        return getattr(attn, name)
+        value = globals()[name] = getattr(attn, name)
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -9,6 +9,7 @@ the current stream of that device unless `stream` is given.
 """
 
 import ctypes
+import struct
 
 import torch
 
@@ -46,12 +47,9 @@ class CacheStruct(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("k", "v", "k_scale", "v_scale")]
 
 
-class RowsStruct(ctypes.Structure):
-    _fields_ = [("p", _vp), ("seq", _i64), ("token", _i64), ("head", _i64)]
-
-
-class SeqsStruct(ctypes.Structure):
-    _fields_ = [("seqs", _i32), ("width", _i32), ("lens", _vp), ("n_new", _vp), ("table", _vp)]
+# mono_rows and mono_seqs of a call, as the bytes that the library reads
+_rows = struct.Struct("@Pqqq").pack
+_seqs = struct.Struct("@iiPPP").pack
 
 
 class AttnInfo(ctypes.Structure):
@@ -105,8 +103,13 @@ def _check(rc):
         raise MonoError(rc, _lib().mono_attn_last_error().decode())
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the current stream's handle, without an object for it
+
+
 def _stream_of(device, stream):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device)
 
 
 def _refuse(who, why):
@@ -140,6 +143,32 @@ def rope(x, positions, rope, out=None, transpose=False, stream=None):
     row, left as it was).  out None rotates in place.  transpose applies the
     transposed map (the gradient's).  Returns out."""
     out = x if out is None else out
+    dev = x.get_device()
+    try:
+        tokens, heads, head_dim = x.shape
+        xt, xh, xd = x.stride()
+        ot, oh, od = out.stride()
+        ok = (dev >= 0 and positions.get_device() == dev and out.get_device() == dev and out.dtype is x.dtype
+              and positions.dtype is torch.int32 and positions.shape == (tokens,) and positions.is_contiguous()
+              and (out is x or out.shape == x.shape) and ((xd == 1 and od == 1) or not tokens or not heads)
+              and x.dtype in _CODE)
+    except ValueError:   # other numbers of dimensions
+        ok = False
+    if not ok:
+        _refuse_rope(x, positions, out)
+    call = (rope._at, tokens, heads, head_dim, _CODE[x.dtype], x.data_ptr(), xt, xh, positions.data_ptr(),
+            out.data_ptr(), ot, oh, 1 if transpose else 0, _stream_of(dev, stream))
+    if torch._C._cuda_getDevice() == dev:
+        rc = _lib().mono_rope_apply(*call)
+    else:
+        with torch.cuda.device(dev):
+            rc = _lib().mono_rope_apply(*call)
+    if rc:
+        _check(rc)
+    return out
+
+
+def _refuse_rope(x, positions, out):
     why = []
     if x.dim() != 3 or positions.dim() != 1 or out.shape != x.shape or positions.shape[0] != x.shape[0]:
         why.append("x and out [tokens][heads][head_dim], positions [tokens]")
@@ -148,21 +177,9 @@ def rope(x, positions, rope, out=None, transpose=False, stream=None):
     if positions.dtype != torch.int32 or not positions.is_contiguous():
         why.append("positions must be contiguous int32")
     dev = x.get_device()
-    if not x.is_cuda or positions.get_device() != dev or out.get_device() != dev:
+    if dev < 0 or positions.get_device() != dev or out.get_device() != dev:
         why.append("every tensor must be on one CUDA device")
-    if not why and x.numel() and (x.stride(2) != 1 or out.stride(2) != 1):
-        why.append("the last dimension must be contiguous")
-    _refuse("rope", why)
-    xs, os = x.stride(), out.stride()
-    tokens, heads, head_dim = x.shape
-    args = (rope._at, tokens, heads, head_dim, _CODE[x.dtype], x.data_ptr(), xs[0], xs[1], positions.data_ptr(),
-            out.data_ptr(), os[0], os[1], 1 if transpose else 0, _stream_of(dev, stream))
-    if torch.cuda.current_device() == dev:
-        _check(_lib().mono_rope_apply(*args))
-    else:
-        with torch.cuda.device(dev):
-            _check(_lib().mono_rope_apply(*args))
-    return out
+    _refuse("rope", why or ["the last dimension must be contiguous"])
 
 
 class KVCache:
@@ -216,22 +233,35 @@ class AttnPlan:
         self.dtype, self.device = _NAME[dtype], device
         self.shape = (num_pages, kv_heads, page_size, head_dim)
         self.q_heads, self.kv_heads, self.head_dim, self.max_pages = q_heads, kv_heads, head_dim, max_pages
+        self._append, self._attend = self._lib.mono_attn_append, self._lib.mono_attn_attend
 
-    def _rows(self, name, x, heads, why):
-        if x.dim() != 4 or x.shape[2] != heads or x.shape[3] != self.head_dim:
-            why.append(f"{name} must be [seqs][width][{heads}][{self.head_dim}]")
-            return None
-        s = x.stride()
-        if s[3] != 1:
-            why.append(f"{name}: the last dimension must be contiguous")
-        if x.dtype != self.dtype or x.get_device() != self.device:
-            why.append(f"{name} must be {self.dtype} on the plan's device")
-        return RowsStruct(x.data_ptr(), s[0], s[1], s[2])
+    def _ok(self, cache, x, heads, y, lens, table, n_new):
+        """Whether a call's tensors are what they must be: x and y rows of `heads`
+        heads, one of each sequence's entries for each row of x."""
+        n, dev = x.shape[0], self.device
+        return (x.dtype is self.dtype and y.dtype is self.dtype and x.get_device() == dev and y.get_device() == dev
+                and x.dim() == 4 and x.shape[2] == heads and x.shape[3] == self.head_dim and y.shape == x.shape
+                and x.stride(3) == 1 and y.stride(3) == 1 and cache.shape == self.shape and cache.device == dev
+                and lens.dtype is torch.int32 and lens.shape == (n,) and lens.get_device() == dev
+                and lens.is_contiguous() and table.dtype is torch.int32 and table.shape == (n, self.max_pages)
+                and table.get_device() == dev and table.is_contiguous()
+                and (n_new is None or (n_new.dtype is torch.int32 and n_new.shape == (n,)
+                                       and n_new.get_device() == dev and n_new.is_contiguous())))
 
-    def _seqs(self, cache, x, lens, table, n_new, why):
-        if cache.shape != self.shape or cache.device != self.device:
+    def _refuse(self, who, names, cache, x, heads, y, lens, table, n_new):
+        why, d = [], self.device
+        for name, t in zip(names, (x, y)):
+            if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != self.head_dim:
+                why.append(f"{name} must be [seqs][width][{heads}][{self.head_dim}]")
+            elif t.stride(3) != 1:
+                why.append(f"{name}: the last dimension must be contiguous")
+            if t.dtype != self.dtype or t.get_device() != d:
+                why.append(f"{name} must be {self.dtype} on the plan's device")
+        if x.shape[:2] != y.shape[:2]:
+            why.append(f"{names[0]} and {names[1]} must have the same rows")
+        if cache.shape != self.shape or cache.device != d:
             why.append(f"the cache must be {list(self.shape)} on the plan's device")
-        n, d = x.shape[0], self.device
+        n = x.shape[0] if x.dim() else 0
         if lens.dtype != torch.int32 or tuple(lens.shape) != (n,) or lens.get_device() != d or not lens.is_contiguous():
             why.append("lens must be contiguous int32 [seqs] on the plan's device")
         if table.dtype != torch.int32 or tuple(table.shape) != (n, self.max_pages) or table.get_device() != d \
@@ -240,39 +270,43 @@ class AttnPlan:
         if n_new is not None and (n_new.dtype != torch.int32 or tuple(n_new.shape) != (n,) or n_new.get_device() != d
                                   or not n_new.is_contiguous()):
             why.append("n_new must be contiguous int32 [seqs] on the plan's device")
-        return SeqsStruct(n, x.shape[1], lens.data_ptr(), None if n_new is None else n_new.data_ptr(), table.data_ptr())
+        _refuse(who, why)
 
     def append(self, cache, k, v, lens, table, rope=None, n_new=None, stream=None):
         """mono_attn_append: k, v [seqs][width][kv_heads][head_dim] (strides free)
         into the pages of `table` [seqs][max_pages]; lens [seqs] counts the new
         tokens, n_new [seqs] says how many of the rows are new (None: all).
         rope: the keys are rotated to their positions on the way."""
-        why = []
-        kr, vr = self._rows("k", k, self.kv_heads, why), self._rows("v", v, self.kv_heads, why)
-        if not why and v.shape[:2] != k.shape[:2]:
-            why.append("k and v must have the same rows")
-        s = self._seqs(cache, k, lens, table, n_new, why) if kr is not None else None
-        _refuse("append", why)
-        _check(self._lib.mono_attn_append(self.handle, cache._at, ctypes.addressof(s), ctypes.addressof(kr),
-                                          ctypes.addressof(vr), None if rope is None else rope._at,
-                                          _stream_of(self.device, stream)))
+        if k.dim() != 4 or not self._ok(cache, k, self.kv_heads, v, lens, table, n_new):
+            self._refuse("append", ("k", "v"), cache, k, self.kv_heads, v, lens, table, n_new)
+        n, width, _, _ = k.shape
+        ks, kt, kh, _ = k.stride()
+        vs, vt, vh, _ = v.stride()
+        rc = self._append(self.handle, cache._at,
+                          _seqs(n, width, lens.data_ptr(), 0 if n_new is None else n_new.data_ptr(), table.data_ptr()),
+                          _rows(k.data_ptr(), ks, kt, kh), _rows(v.data_ptr(), vs, vt, vh),
+                          None if rope is None else rope._at, _stream_of(self.device, stream))
+        if rc:
+            _check(rc)
 
     def attend(self, cache, q, lens, table, out, lse=None, n_new=None, stream=None):
         """mono_attn_attend: out [seqs][width][q_heads][head_dim] of q (rotated; the
         same shape, strides free) over the cached tokens that each row sees.  lse:
         fp32 [seqs][width][q_heads], the log of the sum of exponentials.  Returns out."""
-        why = []
-        qr, orow = self._rows("q", q, self.q_heads, why), self._rows("out", out, self.q_heads, why)
-        if not why and out.shape[:2] != q.shape[:2]:
-            why.append("q and out must have the same rows")
+        if q.dim() != 4 or not self._ok(cache, q, self.q_heads, out, lens, table, n_new):
+            self._refuse("attend", ("q", "out"), cache, q, self.q_heads, out, lens, table, n_new)
+        n, width, _, _ = q.shape
         if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous()
                                 or lse.get_device() != self.device):
-            why.append("lse must be contiguous fp32 [seqs][width][q_heads] on the plan's device")
-        s = self._seqs(cache, q, lens, table, n_new, why) if qr is not None else None
-        _refuse("attend", why)
-        _check(self._lib.mono_attn_attend(self.handle, cache._at, ctypes.addressof(s), ctypes.addressof(qr),
-                                          ctypes.addressof(orow), None if lse is None else lse.data_ptr(),
-                                          _stream_of(self.device, stream)))
+            raise ValueError("attend: lse must be contiguous fp32 [seqs][width][q_heads] on the plan's device")
+        qs, qt, qh, _ = q.stride()
+        os, ot, oh, _ = out.stride()
+        rc = self._attend(self.handle, cache._at,
+                          _seqs(n, width, lens.data_ptr(), 0 if n_new is None else n_new.data_ptr(), table.data_ptr()),
+                          _rows(q.data_ptr(), qs, qt, qh), _rows(out.data_ptr(), os, ot, oh),
+                          None if lse is None else lse.data_ptr(), _stream_of(self.device, stream))
+        if rc:
+            _check(rc)
         return out
 
     def query_error(self):
@@ -323,6 +357,7 @@ class Projection:
         self.dtype, self.device = _NAME[dtype], device
         self.scale_dtype = torch.uint8 if mx else _NAME[scale_dtype]
         self.n_out, self.n_in, self.group, self.zeros = n_out, n_in, group, bool(zeros)
+        self._step = self._lib.mono_proj_step
 
     def pack(self, codes, scales, zeros=None, stream=None):
         """codes uint8 [n_out][n_in / 2] (the even input in the low nibble), scales
@@ -345,19 +380,28 @@ class Projection:
 
     def step(self, x, y, stream=None):
         """y [rows][n_out] = x [rows][n_in] W^T, up to 8 rows, row strides free.  Returns y."""
+        dev = self.device
+        if not (x.dtype is self.dtype and y.dtype is self.dtype and x.get_device() == dev and y.get_device() == dev
+                and x.dim() == 2 and x.shape[1] == self.n_in and y.shape == (x.shape[0], self.n_out)
+                and x.stride(1) == 1 and (y.stride(1) == 1 or self.n_out == 1)):
+            self._refuse_step(x, y)
+        rc = self._step(self.handle, x.shape[0], x.data_ptr(), x.stride(0), y.data_ptr(), y.stride(0),
+                        _stream_of(dev, stream))
+        if rc:
+            _check(rc)
+        return y
+
+    def _refuse_step(self, x, y):
         why = []
         if x.dim() != 2 or x.shape[1] != self.n_in or tuple(y.shape) != (x.shape[0], self.n_out):
             why.append(f"x must be [rows][{self.n_in}] and y [rows][{self.n_out}]")
-        elif (x.stride(1) != 1 and self.n_in > 1) or (y.stride(1) != 1 and self.n_out > 1):
+        elif x.stride(1) != 1 or (y.stride(1) != 1 and self.n_out > 1):
             why.append("the last dimension must be contiguous")
         if x.dtype != self.dtype or y.dtype != self.dtype:
             why.append(f"x and y must be {self.dtype}")
         if x.get_device() != self.device or y.get_device() != self.device:
             why.append("x and y must be on the plan's device")
         _refuse("step", why)
-        _check(self._lib.mono_proj_step(self.handle, x.shape[0], x.data_ptr(), x.stride(0), y.data_ptr(), y.stride(0),
-                                        _stream_of(self.device, stream)))
-        return y
 
     def info(self):
         inf = ProjInfo()

@@ -53,16 +53,18 @@ struct OnDevice {
 
 size_t elem(int dtype) { return dtype == MONO_BF16 ? 2 : 4; }
 
-int check_device(int device, std::string* why, cudaDeviceProp* prop) {
-  int n = 0;
+int check_device(int device, std::string* why, int* sms) {
+  int n = 0, major = 0, minor = 0;
   if (cudaGetDeviceCount(&n) != cudaSuccess || n == 0) *why += "no CUDA device\n";
   else if (device < 0 || device >= n) *why += "device ordinal out of range\n";
   if (!why->empty()) return fail(MONO_ERR_INVALID_ARG, *why);
-  cudaError_t e = cudaGetDeviceProperties(prop, device);
-  if (e != cudaSuccess) return cuda_fail(e, "device properties");
-  if (prop->major != 10 || prop->minor != 0)
-    return fail(MONO_ERR_UNSUPPORTED_ARCH, "device " + std::to_string(device) + " is sm_" + std::to_string(prop->major) +
-                                               std::to_string(prop->minor) + "; this library is built for sm_100a only");
+  cudaError_t e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, device);
+  if (e != cudaSuccess) return cuda_fail(e, "device attributes");
+  if (major != 10 || minor != 0)
+    return fail(MONO_ERR_UNSUPPORTED_ARCH, "device " + std::to_string(device) + " is sm_" + std::to_string(major) +
+                                               std::to_string(minor) + "; this library is built for sm_100a only");
   return MONO_OK;
 }
 
@@ -327,15 +329,15 @@ extern "C" int mono_attn_plan(const mono_attn_config* c, mono_attn_plan_t** out)
       const double tiles = (double)c->max_seqs * c->kv_heads * r.blocks * ((double)c->max_pages * c->page_size / tile + 2);
       need(tiles < 2147483648.0, "max_seqs x kv_heads x max_pages x page_size too large for the 32-bit work partition");
     }
-    cudaDeviceProp prop{};
-    const int rc = check_device(c->device, &why, &prop);
+    int sms = 0;
+    const int rc = check_device(c->device, &why, &sms);
     if (rc) return rc;
     OnDevice on(c->device);
     mono_attn_plan_t* p = new mono_attn_plan_s();
     p->cfg = *c;
     if (p->cfg.scale == 0.f) p->cfg.scale = (float)(1.0 / std::sqrt((double)c->head_dim));
     while ((1 << p->page_shift) < c->page_size) ++p->page_shift;
-    p->sms = prop.multiProcessorCount;
+    p->sms = sms;
     cudaError_t e = cudaFuncSetAttribute(append_for(c->dtype == MONO_F32, append_vecs(c->page_size, c->head_dim)),
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, 56 * 1024);
     size_t rows_max = 0;   // grid x rows of a CTA
@@ -534,10 +536,11 @@ extern "C" int mono_attn_get_info(const mono_attn_plan_t* p, mono_attn_info* inf
 
 struct mono_proj_plan_s {
   mono_proj_config cfg{};
-  int kblocks = 0, groups = 0, nblocks = 0, cluster = 1, sms = 0, sc = 0;
+  int kblocks = 0, groups = 0, nblocks = 0, cluster = 1, teams = 1, sms = 0, sc = 0;
   uint8_t* codes = nullptr;
   uint8_t* scales = nullptr;
   uint8_t* zeros = nullptr;
+  unsigned int* special = nullptr;
   int64_t packed = 0;
   bool is_packed = false;
 };
@@ -552,9 +555,19 @@ ProjFn proj_pick(int sc, bool zp) {
   return zp ? &proj_kernel<F32, kScaleBf16, true> : &proj_kernel<F32, kScaleBf16, false>;
 }
 ProjFn proj_for(bool f32, int sc, bool zp) { return f32 ? proj_pick<true>(sc, zp) : proj_pick<false>(sc, zp); }
-size_t proj_smem_of(bool f32, int rows, int kb) { return f32 ? proj_smem<true>(rows, kb) : proj_smem<false>(rows, kb); }
+using ProjSmemFn = size_t (*)(int, int);
+template <bool F32>
+ProjSmemFn proj_smem_pick(int sc, bool zp) {
+  if (sc == kScaleE8m0) return &proj_smem<F32, kScaleE8m0, false>;
+  if (sc == kScaleF32) return zp ? &proj_smem<F32, kScaleF32, true> : &proj_smem<F32, kScaleF32, false>;
+  return zp ? &proj_smem<F32, kScaleBf16, true> : &proj_smem<F32, kScaleBf16, false>;
+}
+size_t proj_smem_of(bool f32, int sc, bool zp, int rows, int kb) {
+  return (f32 ? proj_smem_pick<true>(sc, zp) : proj_smem_pick<false>(sc, zp))(rows, kb);
+}
 
-constexpr size_t kProjSmemMax = 113 * 1024;   // two CTAs an SM
+constexpr double kProjSumCost = 4, kProjPushCost = 7;   // of an output block's sums, in blocks of a warp
+constexpr size_t kProjSmemMax = 227 * 1024;
 
 }  // namespace
 
@@ -565,6 +578,7 @@ extern "C" void mono_proj_destroy(mono_proj_plan_t* p) {
     cudaFree(p->codes);
     cudaFree(p->scales);
     cudaFree(p->zeros);
+    cudaFree(p->special);
   }
   delete p;
 }
@@ -587,28 +601,40 @@ extern "C" int mono_proj_plan(const mono_proj_config* c, mono_proj_plan_t** out)
     need(!mx || !c->zeros, "MONO_MXFP4 has no zeros");
     need(f32 || c->dtype == MONO_BF16, "dtype must be MONO_F32 or MONO_BF16");
     const int kblocks = c->n_in / 32;
-    const int limit = why.empty() ? (int)((kProjSmemMax - proj_smem_of(f32, 8, 0)) / (8 * 64 * (f32 ? 2 : 1))) : 1;
+    const int sc = mx ? kScaleE8m0 : c->scale_dtype == MONO_F32 ? kScaleF32 : kScaleBf16;
+    int limit = 1;   // blocks of a CTA that fit its shared memory
+    while (why.empty() && proj_smem_of(f32, sc, c->zeros != 0, 8, limit + 1) <= kProjSmemMax) ++limit;
     need((kblocks + 7) / 8 <= limit, "n_in too large: " + std::to_string(limit * 8 * 32) + " at most for this dtype");
-    cudaDeviceProp prop{};
-    const int rc = check_device(c->device, &why, &prop);
+    int sms = 0;
+    const int rc = check_device(c->device, &why, &sms);
     if (rc) return rc;
     OnDevice on(c->device);
     mono_proj_plan_t* p = new mono_proj_plan_s();
     p->cfg = *c;
-    p->sms = prop.multiProcessorCount;
+    p->sms = sms;
     p->kblocks = kblocks;
     p->groups = c->n_in / c->group;
     p->nblocks = (c->n_out + kProjN - 1) / kProjN;
-    p->sc = mx ? kScaleE8m0 : c->scale_dtype == MONO_F32 ? kScaleF32 : kScaleBf16;
-    // the inputs are cut among a cluster until two CTAs an SM have work, as long as each keeps 8 blocks or more
-    while (p->cluster < 8 && ((kblocks + p->cluster - 1) / p->cluster > limit ||
-                              (p->nblocks * p->cluster < 2 * p->sms && kblocks / (2 * p->cluster) >= kProjWarps)))
-      p->cluster *= 2;
+    p->sc = sc;
+    // The inputs are cut among a cluster, or a CTA's warps into teams, where that
+    // shortens the longest run of a warp: rounds over the output blocks x (a
+    // warp's blocks of each + what the sums of a round cost).
+    double best = 1e30;
+    auto offer = [&](int cluster, int teams) {
+      const int kb = (kblocks + cluster - 1) / cluster, slots = p->sms / cluster * teams, tw = kProjWarps / teams;
+      if (kb > limit) return;
+      const double cost = (double)((p->nblocks + slots - 1) / slots) *
+                          ((kb + tw - 1) / tw + (cluster > 1 ? kProjPushCost : kProjSumCost));
+      if (cost < best) best = cost, p->cluster = cluster, p->teams = teams;
+    };
+    for (int x = 1; x <= 8; x *= 2) offer(x, 1);
+    offer(1, 2);
     const size_t sb = p->sc == kScaleBf16 ? 2 : p->sc == kScaleF32 ? 4 : 1;
     const size_t n64 = (size_t)p->nblocks * p->groups * kProjN;
     cudaError_t e = dalloc(&p->codes, (size_t)p->nblocks * kblocks * 1024, &p->packed);
     if (e == cudaSuccess) e = dalloc(&p->scales, n64 * sb, &p->packed);
     if (e == cudaSuccess && c->zeros) e = dalloc(&p->zeros, n64, &p->packed);
+    if (e == cudaSuccess && mx) e = dalloc(&p->special, 4, &p->packed);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(proj_for(f32, p->sc, c->zeros != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)kProjSmemMax);
@@ -637,18 +663,22 @@ extern "C" int mono_proj_pack(mono_proj_plan_t* p, const void* codes, const void
     auto grid = [&](long long n) { return (unsigned)std::min<long long>((n + 255) / 256, 148LL * 64); };
     pack_proj_codes_kernel<<<grid(words), 256, 0, st>>>((const uint8_t*)codes, (uint32_t*)p->codes, p->cfg.n_out,
                                                          p->cfg.n_in, words, p->cfg.format == MONO_MXFP4);
+    if (p->special) {
+      const cudaError_t e = cudaMemsetAsync(p->special, 0, 4, st);
+      if (e != cudaSuccess) return cuda_fail(e, "proj_pack");
+    }
     if (p->sc == kScaleBf16)
       pack_proj_groups_kernel<<<grid(n64), 256, 0, st>>>((const uint16_t*)scales, (uint16_t*)p->scales, p->cfg.n_out,
-                                                          p->groups, n64, 0);
+                                                          p->groups, n64, 0, nullptr);
     else if (p->sc == kScaleF32)
       pack_proj_groups_kernel<<<grid(n64), 256, 0, st>>>((const uint32_t*)scales, (uint32_t*)p->scales, p->cfg.n_out,
-                                                          p->groups, n64, 0);
+                                                          p->groups, n64, 0, nullptr);
     else
       pack_proj_groups_kernel<<<grid(n64), 256, 0, st>>>((const uint8_t*)scales, p->scales, p->cfg.n_out, p->groups,
-                                                          n64, 0);
+                                                          n64, 0, p->special);
     if (zeros)
       pack_proj_groups_kernel<<<grid(n64), 256, 0, st>>>((const uint8_t*)zeros, p->zeros, p->cfg.n_out, p->groups, n64,
-                                                          15);
+                                                          15, nullptr);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "proj_pack");
     p->is_packed = true;
@@ -675,6 +705,7 @@ extern "C" int mono_proj_step(mono_proj_plan_t* p, int rows, const void* x, int6
     a.codes = p->codes;
     a.scales = p->scales;
     a.zeros = p->zeros;
+    a.special = p->special;
     a.x = x;
     a.y = y;
     a.x_row = x_row;
@@ -686,11 +717,18 @@ extern "C" int mono_proj_step(mono_proj_plan_t* p, int rows, const void* x, int6
     a.groups = p->groups;
     a.nblocks = p->nblocks;
     a.x_vec = aligned(x, 16) && x_row % (int64_t)(16 / el) == 0;
-    const int clusters = std::min(p->nblocks, std::max(1, 2 * p->sms / p->cluster));
+    auto log2_of = [](int v) {
+      int l = 0;
+      while ((1 << l) < v) ++l;
+      return l;
+    };
+    a.teams_log2 = log2_of(p->teams);
+    a.cluster_log2 = log2_of(p->cluster);
+    const int clusters = std::min((p->nblocks + p->teams - 1) / p->teams, p->sms / p->cluster);
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3(clusters * p->cluster);
     lc.blockDim = dim3(kProjThreads);
-    lc.dynamicSmemBytes = proj_smem_of(f32, rows, (p->kblocks + p->cluster - 1) / p->cluster);
+    lc.dynamicSmemBytes = proj_smem_of(f32, p->sc, p->zeros != nullptr, rows, (p->kblocks + p->cluster - 1) / p->cluster);
     lc.stream = (cudaStream_t)stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

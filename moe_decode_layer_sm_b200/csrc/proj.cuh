@@ -2,6 +2,8 @@
 #pragma once
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "kv_attend.cuh"
 
 namespace mono {
@@ -15,12 +17,16 @@ struct ProjParams {
   const void* x;
   void* y;
   long long x_row, y_row;
+  const unsigned int* special;   // MXFP4: nonzero where a scale byte is 0 or 255
   int rows, n_out, kblocks, blocks_per_group, groups, nblocks, x_vec;
+  int teams_log2;     // output blocks that a CTA works on at once, each with kProjWarps / teams warps
+  int cluster_log2;   // CTAs that share an output block's inputs
 };
 
-constexpr int kProjWarps = 8, kProjThreads = 32 * kProjWarps;
+constexpr int kProjWarpsLog2 = 4, kProjWarps = 1 << kProjWarpsLog2, kProjThreads = 32 * kProjWarps;
 constexpr int kProjN = 64;      // outputs a block
 constexpr int kProjDepth = 4;   // 32-input blocks that a warp has in flight
+constexpr int kProjRedRow = 68; // floats between the rows of a warp's sums: the lanes' banks 8 t + g
 
 // Packed codes: [nblock][kblock][tile pair 2][lane 32][16 bytes], a lane's 16
 // bytes the words (tile 2h, step 0), (2h, 1), (2h + 1, 0), (2h + 1, 1).  For
@@ -29,7 +35,7 @@ constexpr int kProjDepth = 4;   // 32-input blocks that a warp has in flight
 // assignment of inputs to the MMA's k indices will do as long as x follows it,
 // and this one gives a lane 8 consecutive inputs of x (one 16-byte load).
 //   int4:  nibble j + 4 u of the word = (output g + 8 (j & 1), input k + 2 (j >> 1) + u),
-//          so that two masks and one shift leave the four fp16 pairs of the fragment
+//          so that masks and one shift leave the four fp16 pairs of the fragment
 //   e2m1:  byte j = fragment register j, low nibble first (the pair converter's order)
 __global__ void pack_proj_codes_kernel(const uint8_t* __restrict__ src, uint32_t* __restrict__ dst, int n_out, int n_in,
                                        long long words, int mx) {
@@ -58,7 +64,7 @@ __global__ void pack_proj_codes_kernel(const uint8_t* __restrict__ src, uint32_t
 // lane's eight values of a group lie together.
 template <typename T>
 __global__ void pack_proj_groups_kernel(const T* __restrict__ src, T* __restrict__ dst, int n_out, int groups,
-                                        long long total, int mask) {
+                                        long long total, int mask, unsigned int* special) {
   for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
        i += (long long)gridDim.x * blockDim.x) {
     const int e = i & 1, tile = (i >> 1) & 3, g = (i >> 3) & 7;
@@ -68,256 +74,386 @@ __global__ void pack_proj_groups_kernel(const T* __restrict__ src, T* __restrict
     T v = T(0);
     if (n < n_out) v = src[n * groups + gr];
     if (mask) v = T((int)v & mask);
+    if (special && n < n_out && (v == T(0) || v == T(255))) atomicOr(special, 1u);
     dst[i] = v;
   }
 }
 
+// D = A B, from zero
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// a lane's eight scales of a group: outputs g and g + 8 of each tile
 template <int SC>
 struct ScaleRegs {
-  uint32_t w[SC == kScaleBf16 ? 4 : SC == kScaleF32 ? 8 : 2];
   static constexpr int kBytes = SC == kScaleBf16 ? 2 : SC == kScaleF32 ? 4 : 1;
-  __device__ __forceinline__ void load(const uint8_t* p) {
+  uint32_t w[2 * kBytes];
+  __device__ __forceinline__ void load(const unsigned char* p) {
     if (SC == kScaleE8m0) {
-      const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 a = *reinterpret_cast<const uint2*>(p);
       w[0] = a.x, w[1] = a.y;
     } else {
 #pragma unroll
-      for (int i = 0; i < (SC == kScaleBf16 ? 1 : 2); ++i) {
-        const uint4 a = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        w[4 * i] = a.x, w[4 * i + 1] = a.y, w[(4 * i + 2) % (sizeof(w) / 4)] = a.z, w[(4 * i + 3) % (sizeof(w) / 4)] = a.w;
+      for (int i = 0; i < kBytes / 2; ++i) {
+        const uint4 a = reinterpret_cast<const uint4*>(p)[i];
+        w[(4 * i) % (2 * kBytes)] = a.x, w[(4 * i + 1) % (2 * kBytes)] = a.y;
+        w[(4 * i + 2) % (2 * kBytes)] = a.z, w[(4 * i + 3) % (2 * kBytes)] = a.w;
       }
     }
   }
-  // of output g + 8 e of tile i
+  // of output g + 8 e of tile i; e8m0 by the exponent field alone, which is not what 0 and 255 stand for
   __device__ __forceinline__ float get(int i, int e) const {
-    if (SC == kScaleF32) return __uint_as_float(w[2 * i + e]);
-    if (SC == kScaleBf16) return e ? bf16hi(w[i]) : bf16lo(w[i]);
-    const uint32_t b = (w[i >> 1] >> (16 * (i & 1) + 8 * e)) & 0xFFu;
-    return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23);
+    if (SC == kScaleF32) return __uint_as_float(w[(2 * i + e) % (2 * kBytes)]);
+    if (SC == kScaleBf16) return e ? bf16hi(w[i % (2 * kBytes)]) : bf16lo(w[i % (2 * kBytes)]);
+    const int at = 16 * (i & 1) + 8 * e;
+    return __uint_as_float((at < 24 ? w[i >> 1] << (23 - at) : w[i >> 1] >> 1) & 0x7F800000u);
   }
 };
 
-template <bool F32>
-size_t proj_smem(int rows, int kblocks) {
-  return (size_t)kblocks * rows * 64 * (F32 ? 2 : 1) + 2 * kProjWarps * 32 * 16 * 4 + 512 * 4 + 64;
+__device__ __forceinline__ float e8m0_ends(float s) {   // 2^-127 and NaN
+  const uint32_t b = __float_as_uint(s);
+  return b == 0u ? __uint_as_float(0x00400000u) : b == 0x7F800000u ? __uint_as_float(0x7FC00000u) : s;
 }
 
-// A cluster of CTAs cuts the inputs; each CTA keeps its part of x in shared
-// memory as fp16 (each row scaled by a power of two, fp32 rows as two terms)
-// and walks over output blocks; its 8 warps cut the part again.  Weights go
-// from global memory to registers, kProjDepth blocks ahead and across output
-// blocks, and become exact fp16 operands (int4: the bits under the exponent of
-// 1024 or 64; e2m1: the pair converter); a scale multiplies the fp32 sum of
-// its 32 products.  The warps' sums are added in a fixed order, then the
-// cluster's through distributed shared memory: no scratch, no atomics.
-// Bound by the stream of weights: half a byte and 2 x rows operations each.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int SC, bool ZP>
+__host__ __device__ constexpr int proj_slot() {   // bytes of a block in a warp's ring: codes, scales, zeros
+  return 1024 + 64 * ScaleRegs<SC>::kBytes + (ZP ? 64 : 0);
+}
+
+// shared memory of a CTA with kb blocks of inputs
 template <bool F32, int SC, bool ZP>
-__global__ void __launch_bounds__(kProjThreads, 2) proj_kernel(const ProjParams p) {
+size_t proj_smem(int rows, int kb) {
+  return (size_t)kProjWarps * kProjDepth * proj_slot<SC, ZP>() + (size_t)kb * rows * 64 * (F32 ? 2 : 1) +
+         (SC == kScaleE8m0 ? 0 : (size_t)kb * 32) + (size_t)kProjWarps * (rows * kProjRedRow + 8) * 4 + 2 * 512 * 4;
+}
+
+// A cluster of CTAs cuts the inputs and the warps of a team cut a CTA's part
+// again; a CTA (one an SM) walks over output blocks, one for each team.  Each
+// warp streams its weights through a ring of its own in shared memory by
+// asynchronous copies, kProjDepth blocks ahead and across output blocks: in
+// registers the same depth stalled, since a warp's few scoreboards tie the
+// loads of different blocks together (224 us for 131072 x 5120 MXFP4, 8 rows).
+// x is converted once a CTA, each row of a warp's part scaled by a power of
+// two to fp16's range (fp32 as two terms).  Codes become exact fp16 operands:
+//   e2m1   by the pair converter
+//   int4   by masking: a code in the low bits of a half is the subnormal
+//          q 2^-24, one nibble further up q 2^-20, which the tensor cores
+//          take at full rate; the zero point comes off the group's sum,
+//          sum (q - z) x = sum q x - z sum x, with sum x found once
+// so an int4 code costs half a mask and no conversion.  A group's scale
+// multiplies the fp32 sum of its products.  The warps' sums are added in a
+// fixed order, then the cluster's, pushed to the CTA that writes the output:
+// no scratch, no atomics.
+template <bool F32, int SC, bool ZP>
+__global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_constant__ ProjParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   constexpr bool MX = SC == kScaleE8m0;
-  constexpr int kSplit = F32 ? 2 : 1;
+  constexpr int kSplit = F32 ? 2 : 1, kSlot = proj_slot<SC, ZP>(), SB = ScaleRegs<SC>::kBytes;
   extern __shared__ __align__(16) unsigned char smem[];
-  const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int cs = 1 << p.cluster_log2, rank = (int)cluster.block_rank(), teams = 1 << p.teams_log2;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int kb0 = (int)((long long)p.kblocks * rank / cs), kb1 = (int)((long long)p.kblocks * (rank + 1) / cs);
-  const int kbs = kb1 - kb0, kb_max = (p.kblocks + cs - 1) / cs, R = p.rows;
-  uint4* xs = reinterpret_cast<uint4*>(smem);   // [split][kb][row][t] 8 halves
-  float* red = reinterpret_cast<float*>(smem + (size_t)kb_max * R * 64 * kSplit);   // [2][warp][lane][16]
-  float* part = red + 2 * kProjWarps * 32 * 16;                                     // [512]
-  float* unscale = part + 512;                                                      // [8]
-  const int w0 = kbs * warp / kProjWarps, w1 = kbs * (warp + 1) / kProjWarps, wn = w1 - w0;
-  const int nclusters = gridDim.x / cs, cl = blockIdx.x / cs;
+  const int tw_log2 = kProjWarpsLog2 - p.teams_log2, tw = 1 << tw_log2;   // warps of a team
+  const int team = warp >> tw_log2, kw = warp & (tw - 1);
+  const int kb0 = p.kblocks * rank >> p.cluster_log2, kb1 = p.kblocks * (rank + 1) >> p.cluster_log2;
+  const int kbs = kb1 - kb0, kb_max = (p.kblocks + cs - 1) >> p.cluster_log2, R = p.rows;
+  unsigned char* ring = smem + (size_t)warp * kProjDepth * kSlot;
+  uint4* xs = reinterpret_cast<uint4*>(smem + (size_t)kProjWarps * kProjDepth * kSlot);   // [split][kb][row][t] 8 halves
+  float* xsum = reinterpret_cast<float*>(xs + (size_t)kb_max * R * 4 * kSplit);           // [kb][8 rows], int4
+  float* unscale = xsum + (MX ? 0 : kb_max * 8);          // [kw][8 rows]
+  float* part = unscale + kProjWarps * 8;                 // [turn][rank][512 / cs]
+  float* red = part + 2 * 512 + team * tw * R * kProjRedRow;   // [kw][row][output 64]
+  const int w0 = kbs * kw >> tw_log2, w1 = kbs * (kw + 1) >> tw_log2, wn = w1 - w0;
+  const int nclusters = gridDim.x >> p.cluster_log2, cl = blockIdx.x >> p.cluster_log2;
+  const int nb0 = (cl << p.teams_log2) + team, nb_step = nclusters << p.teams_log2;
+  if (cs > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // waited for before the first push
+  const bool special = MX && __ldg(p.special) != 0u;
 
-  // the warp's blocks: output block cl, cl + nclusters, ..., input blocks
-  // [w0, w1) of each, in rounds of kProjDepth (slots behind w1 stay empty)
-  uint4 code[kProjDepth][2];
-  ScaleRegs<SC> sc[kProjDepth];
-  uint2 zp[kProjDepth];
-  int ld_nb = cl, ld_kb = w0;   // the round that is loaded next
-  auto load = [&](int slot) {
-    if (ld_nb < p.nblocks && ld_kb + slot < w1) {
-      const int kb = kb0 + ld_kb + slot;
-      const uint4* at = reinterpret_cast<const uint4*>(p.codes) + ((long long)ld_nb * p.kblocks + kb) * 64 + lane;
-      code[slot][0] = __ldcs(at);
-      code[slot][1] = __ldcs(at + 32);
-      const long long gr = ((long long)ld_nb * p.groups + kb / p.blocks_per_group) * 64 + g * 8;
-      sc[slot].load(p.scales + gr * ScaleRegs<SC>::kBytes);
-      if (ZP) zp[slot] = __ldg(reinterpret_cast<const uint2*>(p.zeros + gr));
+  // the warp's blocks: output block nb0, nb0 + nb_step, ..., input blocks
+  // [w0, w1) of each.  Scales come with the last block of a group, or of the part.
+  const int bpg = MX ? 1 : p.blocks_per_group;
+  const int gr0 = (kb0 + w0) / bpg, in0 = (kb0 + w0) - gr0 * bpg;   // the first block's group, and its place there
+  int ld_nb = wn > 0 ? nb0 : p.nblocks, ld_kb = w0, ld_in = in0, ld_slot = 0;
+  const uint4* ld_code = reinterpret_cast<const uint4*>(p.codes) + ((long long)nb0 * p.kblocks + kb0 + w0) * 64 + lane;
+  // a lane's part of a group's scales: 2 SB bytes; of e8m0 scales and of zeros, 4 bytes by the first two t
+  const int sc_lane = SB == 1 ? g * 8 + (t & 1) * 4 : lane * 2 * SB, zp_lane = g * 8 + (t & 1) * 4;
+  const long long group_at = ((long long)nb0 * p.groups + gr0) * 64;
+  const uint8_t* ld_sc = p.scales + group_at * SB + sc_lane;
+  const uint8_t* ld_zp = p.zeros + group_at + zp_lane;
+  const long long group_step = ((long long)nb_step * p.groups - ((kb0 + w1 - 1) / bpg - gr0)) * 64;   // from the part's last group
+  const uint32_t ring_at = smem_u32(ring);
+  auto issue = [&] {
+    if (ld_nb < p.nblocks) {
+      const uint32_t at = ring_at + ld_slot * kSlot;
+      cp_async<16>(at + lane * 16, ld_code);
+      cp_async<16>(at + 512 + lane * 16, ld_code + 32);
+      const bool part_end = ld_kb == w1 - 1;
+      if (MX || ld_in == bpg - 1 || part_end) {
+        if (SB > 1 || t < 2) cp_async<SB == 4 ? 8 : 4>(at + 1024 + sc_lane, ld_sc);
+        if (ZP && t < 2) cp_async<4>(at + 1024 + 64 * SB + zp_lane, ld_zp);
+        if (!part_end) {
+          ld_sc += 64 * SB;
+          if (ZP) ld_zp += 64;
+          ld_in = -1;
+        }
+      }
+      ld_code += 64, ++ld_in, ++ld_kb;
+      if (part_end) {
+        ld_kb = w0, ld_nb += nb_step, ld_in = in0;
+        ld_code += ((long long)nb_step * p.kblocks - wn) * 64;
+        ld_sc += group_step * SB;
+        if (ZP) ld_zp += group_step;
+      }
     }
-    if (slot == kProjDepth - 1) {
-      ld_kb += kProjDepth;
-      if (ld_kb >= w1) ld_kb = w0, ld_nb += nclusters;
-    }
+    if (++ld_slot == kProjDepth) ld_slot = 0;
+    cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < kProjDepth; ++i) load(i);
+#pragma unroll 1
+  for (int i = 0; i < kProjDepth - 1; ++i) issue();
 
-  // x: warp r takes row r
-  for (int r = warp; r < R; r += kProjWarps) {
-    const long long row = (long long)r * p.x_row + (long long)kb0 * 32;
-    auto get = [&](int k) {
-      return F32 ? __ldg(reinterpret_cast<const float*>(p.x) + row + k)
-                 : __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(p.x) + row + k));
-    };
-    auto get8 = [&](int k, float* v) {
-      if (p.x_vec) {
+  // x of the warp's part; a team takes every p.teams-th row
+  {
+    const long long row0 = (long long)(kb0 + w0) * 32;
+    auto get8 = [&](auto vec, int r, int q, float* v) {
+      const long long at = (long long)r * p.x_row + row0 + q * 8;
+      if (decltype(vec)::value) {
         if (F32) {
-          const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.x) + row + k);
-          const float4 a = __ldg(q), b = __ldg(q + 1);
+          const float4* s = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p.x) + at);
+          const float4 a = __ldg(s), b = __ldg(s + 1);
           v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
         } else {
-          const uint4 a = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.x) + row + k));
+          const uint4 a = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.x) + at));
           v[0] = bf16lo(a.x), v[1] = bf16hi(a.x), v[2] = bf16lo(a.y), v[3] = bf16hi(a.y);
           v[4] = bf16lo(a.z), v[5] = bf16hi(a.z), v[6] = bf16lo(a.w), v[7] = bf16hi(a.w);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = get(k + i);
+        for (int i = 0; i < 8; ++i)
+          v[i] = F32 ? __ldg(reinterpret_cast<const float*>(p.x) + at + i)
+                     : __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(p.x) + at + i));
       }
     };
-    float amax = 0.f;
-    for (int q = lane; q < kbs * 4; q += 32) {
-      float v[8];
-      get8(q * 8, v);
+    // kRows: rows whose loads are in flight together
+    auto convert = [&](auto vec, auto rows) {
+      constexpr int kRows = decltype(rows)::value;
+      for (int r0 = team; r0 < R; r0 += kRows * teams) {
+        float amax[kRows];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-    }
+        for (int i = 0; i < kRows; ++i) amax[i] = 0.f;
+        for (int q = lane; q < wn * 4; q += 32)
 #pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    int e = 14 - ((int)(__float_as_uint(amax) >> 23) - 127);
-    e = amax > 0.f && amax <= 3.402823466e38f ? min(e, 100) : 0;
-    const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-    if (lane == 0) unscale[r] = __uint_as_float((uint32_t)(127 - e) << 23);
-    for (int q = lane; q < kbs * 4; q += 32) {
-      float v[8];
-      get8(q * 8, v);
-      uint32_t hi[4], lo[4];
+          for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i * teams;
+            if (r < R) {
+              float v[8];
+              get8(vec, r, q, v);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) amax[i] = fmaxf(amax[i], fabsf(v[j]));
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+          for (int o = 16; o; o >>= 1) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xFFFFFFFFu, amax[i], o));
+          // 2^e takes the largest magnitude to [2^14, 2^15)
+          int e = 14 - ((int)(__float_as_uint(amax[i]) >> 23) - 127);
+          e = amax[i] > 0.f && amax[i] <= 3.402823466e38f ? min(e, 100) : 0;
+          if (lane == 0 && r0 + i * teams < R)
+            unscale[kw * 8 + r0 + i * teams] = __uint_as_float((uint32_t)(127 - e) << 23);
+          amax[i] = __uint_as_float((uint32_t)(e + 127) << 23);
+        }
+        for (int q0 = 0; q0 < wn * 4; q0 += 32) {
+          const int q = q0 + lane;
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i * teams;
+            if (r < R) {
+              float sum = 0.f;
+              if (q < wn * 4) {
+                float v[8];
+                get8(vec, r, q, v);
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const float a = v[2 * j] * amax[i], b = v[2 * j + 1] * amax[i];
+                  hi[j] = pack_h2(a, b);
+                  const __half2 hh = *reinterpret_cast<const __half2*>(&hi[j]);
+                  lo[j] = F32 ? pack_h2(a - __low2float(hh), b - __high2float(hh)) : 0u;
+                  const __half2 ll = *reinterpret_cast<const __half2*>(&lo[j]);
+                  sum += __low2float(hh) + __high2float(hh);
+                  if (F32) sum += __low2float(ll) + __high2float(ll);
+                }
+                const int at = ((w0 + (q >> 2)) * R + r) * 4 + (q & 3);
+                xs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if (F32) xs[(size_t)kb_max * R * 4 + at] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              }
+              if (!MX) {
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+                if (q < wn * 4 && t == 0) xsum[(w0 + (q >> 2)) * 8 + r] = sum;
+              }
+            }
+          }
+        }
+      }
+    };
+    if (p.x_vec) convert(std::true_type{}, std::integral_constant<int, 4>{});
+    else convert(std::false_type{}, std::integral_constant<int, 1>{});
+    if (teams > 1) __syncthreads();
+    else __syncwarp();
+  }
+
+  int turn = 0, slot = 0;
+  bool waited = cs == 1;
+  for (int nb = nb0; nb < p.nblocks; nb += nb_step, turn ^= 1) {
+    float acc[4][4], sum[4][4];
+    float gx[2] = {0.f, 0.f};   // sum of x over the group, rows 2t and 2t + 1
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = sum[i][j] = 0.f;
+    int in = in0;
+#pragma unroll 1
+    for (int kb = w0; kb < w1; ++kb) {
+      cp_async_wait<kProjDepth - 2>();
+      __syncwarp();   // the other lanes' copies of this block, and their reads of the slot that is filled next
+      issue();
+      const unsigned char* at = ring + slot * kSlot;
+      if (++slot == kProjDepth) slot = 0;
+      uint4 code[2];
+      code[0] = *reinterpret_cast<const uint4*>(at + lane * 16);
+      code[1] = *reinterpret_cast<const uint4*>(at + 512 + lane * 16);
+      uint4 xv[kSplit];
+#pragma unroll
+      for (int sp = 0; sp < kSplit; ++sp) {
+        xv[sp] = make_uint4(0u, 0u, 0u, 0u);
+        if (g < R) xv[sp] = xs[(size_t)sp * kb_max * R * 4 + (kb * R + g) * 4 + t];
+      }
+      if (!MX) {
+        const float2 x2 = *reinterpret_cast<const float2*>(xsum + kb * 8 + 2 * t);
+        gx[0] += x2.x, gx[1] += x2.y;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float a = v[2 * i] * up, b = v[2 * i + 1] * up;
-        hi[i] = pack_h2(a, b);
-        const __half2 hh = *reinterpret_cast<const __half2*>(&hi[i]);
-        lo[i] = F32 ? pack_h2(a - __low2float(hh), b - __high2float(hh)) : 0u;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const uint4 cw = code[i >> 1];
+          const uint32_t w = (i & 1) ? (st ? cw.w : cw.z) : (st ? cw.y : cw.x);
+          uint32_t a[4];
+          if (MX) {
+            asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+                " cvt.rn.f16x2.e2m1x2 %1, b1;\n cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+                : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                : "r"(w));
+          } else {   // outputs g: q 2^-24; g + 8: q 2^-20
+            const uint32_t v = w >> 8;
+            a[0] = w & 0x000F000Fu;
+            a[1] = w & 0x00F000F0u;
+            a[2] = v & 0x000F000Fu;
+            a[3] = v & 0x00F000F0u;
+          }
+#pragma unroll
+          for (int sp = 0; sp < kSplit; ++sp) {
+            const uint32_t b0 = st ? xv[sp].z : xv[sp].x, b1 = st ? xv[sp].w : xv[sp].y;
+            if (MX && st == 0 && sp == 0) mma_f16_first(sum[i], a, b0, b1);
+            else mma_f16(sum[i], a, b0, b1);
+          }
+        }
       }
-      const int at = ((q >> 2) * R + r) * 4 + (q & 3);
-      xs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      if (F32) xs[(size_t)kb_max * R * 4 + at] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-  }
-  __syncthreads();
-
-  int turn = 0;
-  for (int nb = cl; nb < p.nblocks; nb += nclusters, turn ^= 1) {
-    float acc[4][4];
+      const bool last = MX || ++in == bpg;
+      if (MX || last || kb == w1 - 1) {
+        ScaleRegs<SC> sc;
+        sc.load(at + 1024 + g * 8 * SB);
+        if (MX) {
+          float s[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    for (int kb = w0; kb < w1; kb += kProjDepth) {
+          for (int i = 0; i < 8; ++i) s[i] = sc.get(i >> 1, i & 1);
+          if (special) {
 #pragma unroll
-      for (int u = 0; u < kProjDepth; ++u) {
-        if (kb + u >= w1) {
-          load(u);
-          continue;
-        }
-        uint4 xv[kSplit];
+            for (int i = 0; i < 8; ++i) s[i] = e8m0_ends(s[i]);
+          }
 #pragma unroll
-        for (int sp = 0; sp < kSplit; ++sp) {
-          xv[sp] = make_uint4(0u, 0u, 0u, 0u);
-          if (g < R) xv[sp] = xs[(size_t)sp * kb_max * R * 4 + ((kb + u) * R + g) * 4 + t];
-        }
-        float sum[4][4];
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.f;
-          __half2 zlo[2], zhi[2];   // -(1024 + zero), -(64 + zero) of outputs g, g + 8
-          if (!MX) {
+            for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s[2 * i + (j >> 1)], sum[i][j], acc[i][j]);
+        } else {
+          uint2 zp = make_uint2(0u, 0u);
+          if (ZP) zp = *reinterpret_cast<const uint2*>(at + 1024 + 64 * SB + g * 8);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              if (ZP) {
-                const uint32_t z = ((i < 2 ? zp[u].x : zp[u].y) >> (16 * (i & 1) + 8 * e)) & 15u;
-                const uint32_t b = 0xE400E400u | z | (z << 16);   // -(1024 + z)
-                zlo[e] = *reinterpret_cast<const __half2*>(&b);
-                zhi[e] = __hadd2(zlo[e], __floats2half2_rn(960.f, 960.f));
-              } else {
-                zlo[e] = __floats2half2_rn(-1032.f, -1032.f);
-                zhi[e] = __floats2half2_rn(-72.f, -72.f);
+              const float s = sc.get(i, e), up = e ? 1048576.f : 16777216.f;
+              const float z = ZP ? (float)(((i < 2 ? zp.x : zp.y) >> (16 * (i & 1) + 8 * e)) & 15u) : 8.f;
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                acc[i][2 * e + r] = fmaf(s, fmaf(sum[i][2 * e + r], up, -z * gx[r]), acc[i][2 * e + r]);
+                sum[i][2 * e + r] = 0.f;
               }
             }
-          }
-#pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const uint4 cw = code[u][i >> 1];
-            const uint32_t w = (i & 1) ? (st ? cw.w : cw.z) : (st ? cw.y : cw.x);
-            uint32_t a[4];
-            if (MX) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %1;\n cvt.rn.f16x2.e2m1x2 %0, b0;\n}\n"
-                    : "=r"(a[j])
-                    : "r"(w >> (8 * j)));
-            } else {
-              const uint32_t v = w >> 8;
-              const __half2 sixteenth = __floats2half2_rn(0.0625f, 0.0625f);
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {   // outputs g (nibbles 0, 2) and g + 8 (1, 3)
-                const uint32_t r0 = ((j ? w & 0x00F000F0u : w & 0x000F000Fu)) | 0x64006400u;
-                const uint32_t r1 = ((j ? v & 0x00F000F0u : v & 0x000F000Fu)) | 0x64006400u;
-                const __half2 h0 = *reinterpret_cast<const __half2*>(&r0), h1 = *reinterpret_cast<const __half2*>(&r1);
-                const __half2 o0 = j ? __hfma2(h0, sixteenth, zhi[1]) : __hadd2(h0, zlo[0]);
-                const __half2 o1 = j ? __hfma2(h1, sixteenth, zhi[1]) : __hadd2(h1, zlo[0]);
-                a[j] = *reinterpret_cast<const uint32_t*>(&o0);
-                a[2 + j] = *reinterpret_cast<const uint32_t*>(&o1);
-              }
-            }
-#pragma unroll
-            for (int sp = 0; sp < kSplit; ++sp)
-              mma_f16(sum[i], a, st ? xv[sp].z : xv[sp].x, st ? xv[sp].w : xv[sp].y);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sc[u].get(i, j >> 1), sum[i][j], acc[i][j]);
+          gx[0] = gx[1] = 0.f;
+          in = 0;
         }
-        load(u);
       }
     }
     // acc[i][j]: output 16 i + g + 8 (j >> 1), row 2 t + (j & 1)
-    float4* mine = reinterpret_cast<float4*>(red + ((size_t)(turn * kProjWarps + warp) * 32 + lane) * 16);
+    auto team_sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(tw * 32) : "memory"); };
+    if (nb != nb0) team_sync();   // red of the block before is read
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mine[(i + lane) & 3] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-    __syncthreads();
-    // thread: (lane ln, tile i) and two of its four values
+    for (int r = 0; r < 2; ++r)
+      if (2 * t + r < R) {
+        const float un = unscale[kw * 8 + 2 * t + r];
+        float* to = red + (kw * R + 2 * t + r) * kProjRedRow + g;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int idx = tid + half * kProjThreads;   // 512 sums: ln = idx / 16, slot of 4, j
-      const int ln = idx >> 4, slot = (idx >> 2) & 3, j = idx & 3, i = (slot - ln) & 3;
-      float v = 0.f;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int w = 0; w < kProjWarps; ++w) v += red[((size_t)(turn * kProjWarps + w) * 32) * 16 + idx];
-      const int n = nb * kProjN + 16 * i + (ln >> 2) + 8 * (j >> 1), r = 2 * (ln & 3) + (j & 1);
-      v *= r < R ? unscale[r] : 0.f;
-      if (cs == 1) {
-        if (r < R && n < p.n_out) {
-          if (F32) reinterpret_cast<float*>(p.y)[(long long)r * p.y_row + n] = v;
-          else reinterpret_cast<__nv_bfloat16*>(p.y)[(long long)r * p.y_row + n] = __float2bfloat16_rn(v);
-        }
-      } else {
-        part[idx] = v;
+          for (int e = 0; e < 2; ++e) to[16 * i + 8 * e] = acc[i][2 * e + r] * un;
       }
+    team_sync();
+    auto write = [&](int r, int n, float v) {
+      if (n < p.n_out) {
+        if (F32) reinterpret_cast<float*>(p.y)[(long long)r * p.y_row + n] = v;
+        else reinterpret_cast<__nv_bfloat16*>(p.y)[(long long)r * p.y_row + n] = __float2bfloat16_rn(v);
+      }
+    };
+    if (!waited) {
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      waited = true;
+    }
+    const int slice_log2 = 6 - p.cluster_log2, slice = 1 << slice_log2;   // of a block's outputs, for each CTA to finish
+    for (int idx = tid - team * tw * 32; idx < R * kProjN; idx += tw * 32) {
+      const int r = idx >> 6, n = idx & 63;
+      float v = 0.f;
+#pragma unroll 4
+      for (int w = 0; w < tw; ++w) v += red[(w * R + r) * kProjRedRow + n];
+      if (cs == 1) write(r, nb * kProjN + n, v);
+      else *cluster.map_shared_rank(part + turn * 512 + (rank << (9 - p.cluster_log2)) + r * slice + (n & (slice - 1)), n >> slice_log2) = v;
     }
     if (cs > 1) {
+      // one barrier a block: the other half of part is written before the next
       cluster.sync();
-      for (int idx = rank * kProjThreads + tid; idx < 512; idx += cs * kProjThreads) {
-        const int ln = idx >> 4, slot = (idx >> 2) & 3, j = idx & 3, i = (slot - ln) & 3;
-        const int n = nb * kProjN + 16 * i + (ln >> 2) + 8 * (j >> 1), r = 2 * (ln & 3) + (j & 1);
+      for (int idx = tid; idx < R * slice; idx += kProjThreads) {
         float v = 0.f;
-        for (int c = 0; c < cs; ++c) v += cluster.map_shared_rank(part, c)[idx];
-        if (r < R && n < p.n_out) {
-          if (F32) reinterpret_cast<float*>(p.y)[(long long)r * p.y_row + n] = v;
-          else reinterpret_cast<__nv_bfloat16*>(p.y)[(long long)r * p.y_row + n] = __float2bfloat16_rn(v);
-        }
+        for (int c = 0; c < cs; ++c) v += part[turn * 512 + (c << (9 - p.cluster_log2)) + idx];
+        write(idx >> slice_log2, nb * kProjN + rank * slice + (idx & (slice - 1)), v);
       }
-      cluster.sync();   // part is read
     }
   }
+  cp_async_wait<0>();
+  if (!waited) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace mono
