@@ -28,7 +28,7 @@ struct AppendParams {
   const int* n_new;
   const int* table;
   BadIndex* bad;
-  int width, kv_heads, head_dim, page_shift, num_pages, max_pages, heads_per_cta, rotate, vec_ok;
+  int width, kv_heads, head_dim, head_log2, page_shift, num_pages, max_pages, heads_per_cta, rotate, vec_ok;
   mono_rope rope;
 };
 
@@ -43,10 +43,22 @@ __device__ __forceinline__ float fp8_sticky(double q) {
 }
 
 // whether q, a quotient that is off by less than 4 units in the last place,
-// may lie on the other side of a border between two codes
+// may lie on the other side of a border between two codes: halfway between two
+// mantissas of 3 bits.  Below 2^-6 the codes are as far apart as above it.
 __device__ __forceinline__ bool fp8_near_border(float q) {
-  const int low = (int)(__float_as_uint(q) & 0xFFFFFu) - 0x80000;
-  return (low <= 4 && low >= -4) || fabsf(q) < 0.015625f;
+  float m = fabsf(q);
+  if (m < 0.015625f) m += 0.015625f;
+  return ((__float_as_uint(m) + 0x80008u) & 0xFFFF0u) == 0u;
+}
+
+// q = x / s near a border: on the side of it where the exact quotient lies, or
+// on it.  The border has 5 bits, so the sign of x - border x s is exact.
+__device__ __forceinline__ float fp8_settle(float q, float x, float s) {
+  const float low = fabsf(q) < 0.015625f ? 0.015625f : 0.f;
+  const float b = __uint_as_float((__float_as_uint(fabsf(q) + low) & 0xFFF00000u) | 0x80000u) - low;
+  const float r = fmaf(-b, s, fabsf(x));
+  const uint32_t y = __float_as_uint(b) + (r > 0.f ? 1u : r < 0.f ? 0xFFFFFFFFu : 0u);
+  return __uint_as_float(y | (__float_as_uint(q) & 0x80000000u));
 }
 
 __device__ __forceinline__ uint16_t fp8_pair(float lo, float hi) {
@@ -62,32 +74,46 @@ __device__ __forceinline__ uint2 fp8_pack8(const float* q) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
+// eight values from a row, by one or two 16-byte loads where that is allowed
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, float* v) {
-  if (vec) {
+__device__ __forceinline__ Vec<T, 8> load8(const T* p, bool wide) {
+  Vec<T, 8> v;
+  if (wide) {
     constexpr int N = 16 / sizeof(T);
 #pragma unroll
     for (int i = 0; i < 8 / N; ++i) {
       const Vec<T, N> a = reinterpret_cast<const Vec<T, N>*>(p)[i];
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[i * N + j] = to_f(a.v[j]);
+      for (int j = 0; j < N; ++j) v.v[i * N + j] = a.v[j];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f(p[i]);
+    for (int i = 0; i < 8; ++i) v.v[i] = p[i];
   }
+  return v;
+}
+
+__device__ __forceinline__ double2 turn_by(double2 a, double2 b) {   // angles added
+  return make_double2(a.x * b.x - a.y * b.y, a.y * b.x + a.x * b.y);
+}
+
+__device__ __forceinline__ double2 turn_of(double turns) {
+  double sn, cs;
+  sincospi(2.0 * (turns - rint(turns)), &sn, &cs);
+  return make_double2(cs, sn);
 }
 
 // cos and sin of the tokens of a page in two levels: token t of the new ones is
-// turned by far[t / 8] and then by near[t % 8]
+// turned by far[t / 8] and then by near[t % 8].  A level's pairs lie so that
+// threads which take eight pairs each meet no bank conflict.
 struct Turns {
   const double2* far;
   const double2* near;
-  int half, off;
+  int half, off, step;   // step: (half + 7) / 8
   bool interleaved;
+  __device__ __forceinline__ int slot(int i) const { return (i & 7) * step + (i >> 3); }
   __device__ __forceinline__ double2 at(int t, int i) const {
-    const double2 a = far[(t >> 3) * half + i], b = near[(t & 7) * half + i];
-    return make_double2(a.x * b.x - a.y * b.y, a.y * b.x + a.x * b.y);
+    return turn_by(far[(t >> 3) * 8 * step + slot(i)], near[(t & 7) * 8 * step + slot(i)]);
   }
   // dimension d (rotated) of a token's head
   template <typename T>
@@ -101,19 +127,58 @@ struct Turns {
   }
 };
 
+// The code of dimension d of a token's head, from its exact value; out of
+// line, since few values need it and the kernel's code would not fit the
+// instruction cache with it at every place.
+template <typename T>
+__device__ __noinline__ uint8_t exact_code(const Turns& turns, bool rotated, const T* row, int t, int d, float s) {
+  const double y = rotated ? turns.one(row, t, d) : (double)to_f(row[d]);
+  return (uint8_t)fp8_pair(fp8_sticky(y / (double)s), 0.f);
+}
+
+// the largest finite magnitude of eight values of a token's head
+template <typename T>
+__device__ __noinline__ double finite_max8(const Turns& turns, bool rotate, const T* row, int t, int d) {
+  double most = 0.0;
+#pragma unroll 1
+  for (int e = d; e < d + 8; ++e) {
+    const double m =
+        fabs(rotate && e >= turns.off && e < turns.off + 2 * turns.half ? turns.one(row, t, e) : (double)to_f(row[e]));
+    if (m > most && m < 1e300) most = m;
+  }
+  return most;
+}
+
+// shared memory of `most` new tokens in a page
+__host__ __device__ inline size_t append_smem(int most, int rot_dim) {
+  return (size_t)((most + 7) / 8 + (most < 8 ? most : 8)) * 8 * ((rot_dim / 2 + 7) / 8) * sizeof(double2);
+}
+
+__device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
+  const unsigned int hi = __reduce_max_sync(0xFFFFFFFFu, (unsigned int)(v >> 32));
+  const unsigned int lo = __reduce_max_sync(0xFFFFFFFFu, (unsigned int)(v >> 32) == hi ? (unsigned int)v : 0u);
+  return ((unsigned long long)hi << 32) | lo;
+}
+
 // One CTA: the new tokens of one page of one sequence, for a group of heads
 // of k or of v.  grid (pages a sequence's new tokens can touch, 2 x head
 // groups, sequences).  A page's head is held in registers between the two
 // passes that its scale needs (largest magnitude, then the codes), so the
-// input is read once.  The angles are computed once for all heads of the CTA.
+// input is read once, the next head's while this one's is reduced.
+//
 // The rotation is done in binary64 and a code near a border is found from it
 // again, so codes and scales are those of the exact rotated values: a key's
-// code does not depend on which call, or which neighbours, it was written with.
-// VECS: vectors of 8 values that a thread holds of a page's head.
-template <typename T, int VECS>
+// code does not depend on which call, or which neighbours, it was written
+// with.  Two sines and cosines a pair and page, shared by its heads, give all
+// the others by turning; a thread holds both halves of its pairs, so a value
+// costs one conversion each way and four binary64 operations.
+//
+// U: units of 16 values that a thread holds of a page's head.  EACH: rotations
+// whose offset or halves no vector of eight respects.
+template <typename T, int U, bool EACH>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
-  extern __shared__ __align__(16) unsigned char smem_append[];   // far [tokens / 8][half], near [8][half]
-  __shared__ double red[32];
+  extern __shared__ __align__(16) unsigned char smem_append[];   // near [8][slots], far [tokens / 8][slots]
+  __shared__ unsigned long long red[2][kAppendThreads / 32];
   const int s = blockIdx.z, which = blockIdx.y & 1, hg = blockIdx.y >> 1;
   const int P = 1 << p.page_shift, D = p.head_dim, cap = p.max_pages << p.page_shift;
   const int n_new = p.n_new ? __ldg(p.n_new + s) : p.width;
@@ -134,123 +199,182 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     return;
   }
   const int older = a - (page_no << p.page_shift);   // the page's tokens before the new ones
-  const int vpt = D >> 3;                            // vectors of 8 a token
-  const int half = p.rope.rot_dim >> 1, off = p.rope.offset;
-  const bool rotate = p.rotate && which == 0;
-  Turns turns{nullptr, nullptr, half, off, p.rope.interleaved != 0};
-  if (rotate) {
-    const int n_far = (b - a + 7) >> 3, n_near = min(b - a, 8);
-    double2* far = reinterpret_cast<double2*>(smem_append);
-    double2* near = far + n_far * half;
-    for (int i = threadIdx.x; i < (n_far + n_near) * half; i += blockDim.x) {
-      const int t = i / half, pair = i - t * half;
-      const bool is_far = t < n_far;
-      double x = p.rope.turns[pair] * (double)(is_far ? a + 8 * t : t - n_far);
-      x -= rint(x);
-      double sn, cs;
-      sincospi(2.0 * x, &sn, &cs);
-      const double f = is_far ? (double)p.rope.factor : 1.0;
-      far[i] = make_double2(f * cs, f * sn);
+  const int rot = p.rope.rot_dim, half = rot >> 1, off = p.rope.offset;
+  // how a token's head is cut into units: all rows as they come; (half layout)
+  // eight pairs, the unrotated vectors two by two; (interleaved) 16 in a row
+  enum { kPlain, kHalves, kInterleaved, kEach };
+  const int mode = !p.rotate || which ? kPlain : EACH ? kEach : p.rope.interleaved ? kInterleaved : kHalves;
+  const int upt_log2 = p.head_log2 - 4, nunits = (b - a) << upt_log2;
+  const int h0 = hg * p.heads_per_cta, h1 = min(h0 + p.heads_per_cta, p.kv_heads);
+  const T* x0 = reinterpret_cast<const T*>(p.x[which]) + (long long)s * p.x_seq[which] +
+                (long long)(a - sv.first) * p.x_tok[which];
+
+  int tok[U], da[U], db[U], pair[U];   // token, the two vectors' places, kHalves: first pair or -1
+  bool live[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int idx = threadIdx.x + u * blockDim.x, c = idx & ((1 << upt_log2) - 1);
+    live[u] = idx < nunits;
+    tok[u] = idx >> upt_log2;
+    da[u] = c * 16, db[u] = da[u] + 8, pair[u] = -1;
+    if (!EACH && mode == kHalves) {
+      const int nh = half >> 3, j = 16 * (c - nh);
+      if (c < nh) pair[u] = c * 8, da[u] = off + c * 8, db[u] = da[u] + half;
+      else da[u] = j < off ? j : j + rot, db[u] = j + 8 < off ? j + 8 : j + 8 + rot;
+    }
+  }
+  auto row_of = [&](int h, int u) { return x0 + (long long)h * p.x_head[which] + (long long)tok[u] * p.x_tok[which]; };
+  Vec<T, 8> raw[U][2];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (live[u]) {
+        const T* row = row_of(h, u);
+        raw[u][0] = load8(row + da[u], p.vec_ok);
+        raw[u][1] = load8(row + db[u], p.vec_ok);
+      }
+  };
+  constexpr bool kAhead = U * sizeof(T) <= 8;   // registers for the next head's values
+  if (kAhead) fetch(h0);
+
+  Turns turns{nullptr, nullptr, half, off, (half + 7) >> 3, p.rope.interleaved != 0};
+  if (mode != kPlain) {
+    const int n_far = (b - a + 7) >> 3, n_near = min(b - a, 8), slots = 8 * turns.step;
+    double2* near = reinterpret_cast<double2*>(smem_append);
+    double2* far = near + n_near * slots;
+    for (int i = threadIdx.x; i < 2 * half; i += blockDim.x) {
+      const bool is_far = i < half;
+      const int pr = is_far ? i : i - half;
+      const double f = p.rope.turns[pr];
+      double2 w = make_double2(1.0, 0.0);
+      if (is_far) {
+        w = turn_of(f * (double)a);
+        w.x *= (double)p.rope.factor, w.y *= (double)p.rope.factor;
+      }
+      const int n = is_far ? n_far : n_near;
+      double2* to = (is_far ? far : near) + turns.slot(pr);
+      if (n > 1) {
+        const double2 by = turn_of(is_far ? 8.0 * f : f);
+        for (int k = 0; k < n; ++k, w = turn_by(w, by)) to[k * slots] = w;
+      } else {
+        *to = w;
+      }
     }
     turns.far = far;
     turns.near = near;
     __syncthreads();
   }
-  const int h0 = hg * p.heads_per_cta, h1 = min(h0 + p.heads_per_cta, p.kv_heads);
-  const int nvec = (b - a) * vpt;
+
+  int turn = 0;
   for (int h = h0; h < h1; ++h) {
-    const T* x = reinterpret_cast<const T*>(p.x[which]) + (long long)s * p.x_seq[which] +
-                 (long long)h * p.x_head[which] + (long long)(a - sv.first) * p.x_tok[which];
     float* scale_at = p.scales[which] + (long long)page * p.kv_heads + h;
     const float was = older > 0 ? *scale_at : 0.f;
-    float val[VECS][8];
+    if (!kAhead) fetch(h);
+    float val[U][16];
     double amax = 0.0;
-    auto turned = [&](int d) { return rotate && d >= off && d < off + 2 * half; };
+    float top = 0.f;   // of the values that are not rotated
 #pragma unroll
-    for (int q = 0; q < VECS; ++q) {
-      const int idx = threadIdx.x + q * blockDim.x;
-      if (idx < nvec) {
-        const int t = idx / vpt, d0 = (idx - t * vpt) * 8;
-        const T* row = x + (long long)t * p.x_tok[which];
-        load8(row + d0, p.vec_ok, val[q]);
-        float top = 0.f;   // of the values as they came
-        if (!turned(d0) && !turned(d0 + 7) && (off < d0 || off >= d0 + 8 || !rotate)) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(val[q][i]) <= 3.402823466e38f ? fabsf(val[q][i]) : 0.f);
-          amax = fmax(amax, (double)top);
-        } else if (p.vec_ok && half % 8 == 0 && off % 8 == 0) {
-          const int r = d0 - off;
-          double y[8];
-          if (p.rope.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const double2 cs = turns.at(t, (r + i) >> 1);
-              const double x1 = val[q][i], x2 = val[q][i + 1];
-              y[i] = cs.x * x1 - cs.y * x2;
-              y[i + 1] = cs.y * x1 + cs.x * x2;
-            }
-          } else {
-            const bool low = r < half;
-            float other[8];
-            load8(row + (low ? d0 + half : d0 - half), true, other);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const double2 cs = turns.at(t, (low ? r : r - half) + i);
-              y[i] = cs.x * (double)val[q][i] + (low ? -cs.y : cs.y) * (double)other[i];
-            }
-          }
+    for (int u = 0; u < U; ++u)
+      if (live[u]) {
+        if (!EACH && mode == kHalves && pair[u] >= 0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const double m = fabs(y[i]);
-            if (m > amax && m < 1e300) amax = m;
-            val[q][i] = (float)y[i];
+            const double2 cs = turns.at(tok[u], pair[u] + i);
+            const double x1 = to_f(raw[u][0].v[i]), x2 = to_f(raw[u][1].v[i]);
+            const double y1 = cs.x * x1 - cs.y * x2, y2 = cs.y * x1 + cs.x * x2;
+            amax = fmax(amax, fabs(y1));   // NaN is left out
+            amax = fmax(amax, fabs(y2));
+            val[u][i] = (float)y1, val[u][8 + i] = (float)y2;
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const double y = turned(d0 + i) ? turns.one(row, t, d0 + i) : (double)val[q][i];
-            const double m = fabs(y);
-            if (m > amax && m < 1e300) amax = m;
-            val[q][i] = (float)y;
+          for (int v = 0; v < 2; ++v) {
+            const int d = v ? db[u] : da[u];
+            if (!EACH && mode == kInterleaved && d >= off && d < off + rot) {
+#pragma unroll
+              for (int i = 0; i < 8; i += 2) {
+                const double2 cs = turns.at(tok[u], (d - off + i) >> 1);
+                const double x1 = to_f(raw[u][v].v[i]), x2 = to_f(raw[u][v].v[i + 1]);
+                const double y1 = cs.x * x1 - cs.y * x2, y2 = cs.y * x1 + cs.x * x2;
+                amax = fmax(amax, fabs(y1));   // NaN is left out
+                amax = fmax(amax, fabs(y2));
+                val[u][8 * v + i] = (float)y1, val[u][8 * v + i + 1] = (float)y2;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                float x = to_f(raw[u][v].v[i]);
+                if (EACH && mode == kEach && d + i >= off && d + i < off + rot) {
+                  const double y = turns.one(row_of(h, u), tok[u], d + i);
+                  amax = fmax(amax, fabs(y));
+                  x = (float)y;
+                } else {
+                  top = fmaxf(top, fabsf(x));
+                }
+                val[u][8 * v + i] = x;
+              }
+            }
           }
         }
       }
-    }
+    if (kAhead && h + 1 < h1) fetch(h + 1);
+    // the largest of the page's head; positive doubles order as their bits do
+    amax = fmax(amax, (double)top);
+    auto block_max = [&](unsigned long long v) {
+      v = warp_max(v);
+      if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = v;
+      __syncthreads();   // red has two places: the one after next writes here behind the next barrier
+      v = warp_max((threadIdx.x & 31) < (blockDim.x >> 5) ? red[turn][threadIdx.x & 31] : 0ull);
+      turn ^= 1;
+      return __longlong_as_double((long long)v);
+    };
+    amax = block_max((unsigned long long)__double_as_longlong(amax));
+    if (!(amax < 1e300)) {   // an infinity among them: once more, without
+      amax = 0.0;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmax(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    __syncthreads();   // red of the head before is read
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-    __syncthreads();
-    for (int w = 0; w < (int)blockDim.x >> 5; ++w) amax = fmax(amax, red[w]);
+      for (int u = 0; u < U; ++u)
+        if (live[u]) {
+          amax = fmax(amax, finite_max8(turns, mode != kPlain, row_of(h, u), tok[u], da[u]));
+          amax = fmax(amax, finite_max8(turns, mode != kPlain, row_of(h, u), tok[u], db[u]));
+        }
+      amax = block_max((unsigned long long)__double_as_longlong(amax));
+    }
     float sc = fmaxf((float)(amax / (double)kFp8Max), 1.175494351e-38f);
     if (older > 0) sc = fmaxf(sc, was);
     const float rs = __fdiv_rn(1.f, sc);
     uint8_t* dst = p.codes[which] + code_row(page, p.kv_heads, h, P, 0) * D;
 #pragma unroll
-    for (int q = 0; q < VECS; ++q) {
-      const int idx = threadIdx.x + q * blockDim.x;
-      if (idx < nvec) {
-        bool near = false;
-        float y[8];
+    for (int u = 0; u < U; ++u)
+      if (live[u]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] = val[q][i] * rs;
-          near |= fp8_near_border(y[i]);
-        }
-        if (near) {
-          const int t = idx / vpt, d0 = (idx - t * vpt) * 8;
-          const T* row = x + (long long)t * p.x_tok[which];
+        for (int v = 0; v < 2; ++v) {
+          const int d = v ? db[u] : da[u];
+          uint8_t* to = dst + (older + tok[u]) * D + d;
+          unsigned int near = 0u;
+          float y[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (fp8_near_border(y[i]))
-              y[i] = fp8_sticky((turned(d0 + i) ? turns.one(row, t, d0 + i) : (double)val[q][i]) / (double)sc);
+          for (int i = 0; i < 8; ++i) {
+            y[i] = val[u][8 * v + i] * rs;
+            if (fp8_near_border(y[i])) near |= 1u << i;
+          }
+          // (bf16 values meet borders often: 0.3 % of them, half of a warp's vectors)
+          if (!EACH && near && !(mode == kHalves ? pair[u] >= 0 : mode == kInterleaved && d >= off && d < off + rot)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (near & (1u << i)) y[i] = fp8_settle(y[i], val[u][8 * v + i], sc);
+            near = 0u;
+          }
+          *reinterpret_cast<uint2*>(to) = fp8_pack8(y);
+#pragma unroll 1
+          for (; near; near &= near - 1) {
+            const int e = d + __ffs(near) - 1;
+            to[e - d] = exact_code(turns, mode != kPlain && e >= off && e < off + rot, row_of(h, u), tok[u], e, sc);
+          }
         }
-        *reinterpret_cast<uint2*>(dst + (long long)older * D + idx * 8) = fp8_pack8(y);
       }
-    }
     if (older > 0 && sc > was) {
       const double ratio = (double)was / (double)sc;
-      for (int idx = threadIdx.x; idx < older * vpt; idx += blockDim.x) {
+      for (int idx = threadIdx.x; idx < older << (upt_log2 + 1); idx += blockDim.x) {
         uint2* at = reinterpret_cast<uint2*>(dst + idx * 8);
         const uint2 w = *at;
         float v[8];

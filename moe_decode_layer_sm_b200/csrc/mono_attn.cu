@@ -274,10 +274,14 @@ AttendKernel attend_for(int head_dim, int nt, bool f32) {
 }
 
 using AppendFn = void (*)(AppendParams);
-int append_vecs(int page_size, int head_dim) { return page_size * head_dim > 4 * 8 * kAppendThreads ? 8 : 4; }
-AppendFn append_for(bool f32, int vecs) {
-  if (f32) return vecs == 8 ? &append_kernel<float, 8> : &append_kernel<float, 4>;
-  return vecs == 8 ? &append_kernel<__nv_bfloat16, 8> : &append_kernel<__nv_bfloat16, 4>;
+int append_units(int page_size, int head_dim) { return page_size * head_dim > 2 * 16 * kAppendThreads ? 4 : 2; }
+template <typename T>
+AppendFn append_pick(int units, bool each) {
+  if (units == 4) return each ? &append_kernel<T, 4, true> : &append_kernel<T, 4, false>;
+  return each ? &append_kernel<T, 2, true> : &append_kernel<T, 2, false>;
+}
+AppendFn append_for(bool f32, int units, bool each) {
+  return f32 ? append_pick<float>(units, each) : append_pick<__nv_bfloat16>(units, each);
 }
 
 template <typename T>
@@ -338,8 +342,10 @@ extern "C" int mono_attn_plan(const mono_attn_config* c, mono_attn_plan_t** out)
     if (p->cfg.scale == 0.f) p->cfg.scale = (float)(1.0 / std::sqrt((double)c->head_dim));
     while ((1 << p->page_shift) < c->page_size) ++p->page_shift;
     p->sms = sms;
-    cudaError_t e = cudaFuncSetAttribute(append_for(c->dtype == MONO_F32, append_vecs(c->page_size, c->head_dim)),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, 56 * 1024);
+    cudaError_t e = cudaSuccess;
+    for (int each = 0; each < 2 && e == cudaSuccess; ++each)
+      e = cudaFuncSetAttribute(append_for(c->dtype == MONO_F32, append_units(c->page_size, c->head_dim), each),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, 56 * 1024);
     size_t rows_max = 0;   // grid x rows of a CTA
     const int group = c->q_heads / c->kv_heads;
     int blocks = 1;
@@ -428,6 +434,7 @@ extern "C" int mono_attn_append(mono_attn_plan_t* p, const mono_kv_cache* c, con
     a.width = s->width;
     a.kv_heads = p->cfg.kv_heads;
     a.head_dim = D;
+    a.head_log2 = D == 64 ? 6 : D == 128 ? 7 : 8;
     a.page_shift = p->page_shift;
     a.num_pages = p->cfg.num_pages;
     a.max_pages = p->cfg.max_pages;
@@ -441,11 +448,11 @@ extern "C" int mono_attn_append(mono_attn_plan_t* p, const mono_kv_cache* c, con
       hpc *= 2;
     a.heads_per_cta = hpc;
     const int groups = (p->cfg.kv_heads + hpc - 1) / hpc;
-    const int vecs = append_vecs(P, D), threads = std::max(64, P * D / (8 * vecs));
-    const int most = std::min(P, s->width);   // new tokens of a page
-    const size_t smem = rope ? (size_t)((most + 7) / 8 + std::min(most, 8)) * (rope->rot_dim / 2) * sizeof(double2) : 0;
-    append_for(p->cfg.dtype == MONO_F32, vecs)<<<dim3(spans, 2 * groups, s->seqs), threads, smem,
-                                                 (cudaStream_t)stream>>>(a);
+    const int units = append_units(P, D), threads = std::max(64, P * D / (16 * units));
+    const size_t smem = rope ? append_smem(std::min(P, s->width), rope->rot_dim) : 0;
+    const bool each = rope && ((rope->offset | (rope->interleaved ? rope->rot_dim : rope->rot_dim / 2)) & 7);
+    append_for(p->cfg.dtype == MONO_F32, units, each)<<<dim3(spans, 2 * groups, s->seqs), threads, smem,
+                                                        (cudaStream_t)stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? (int)MONO_OK : cuda_fail(e, "append");
   });
