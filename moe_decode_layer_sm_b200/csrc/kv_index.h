@@ -58,13 +58,14 @@ MONO_HD long long code_row(int page, int kv_heads, int h, int page_size, int tok
   return ((long long)page * kv_heads + h) * page_size + tok;
 }
 
-// tiles of `tile` tokens that a sequence's rows read; at least one for a live
-// sequence, whose rows have to be written even if they see nothing
-MONO_HD int seq_tiles(const SeqView& v, int window, int cap, int tile) {
+// length on the line of a sequence's item: `lead` for its start and the tiles
+// of `tile` tokens that its rows read; at least one tile for a live sequence,
+// whose rows have to be written even if they see nothing
+MONO_HD int seq_tiles(const SeqView& v, int window, int cap, int tile, int lead) {
   if (v.n == 0) return 0;
   const int lo = row_lo(v, 0, window), hi = row_hi(v, v.n - 1, cap);
-  if (hi <= lo) return 1;
-  return (hi - 1) / tile - lo / tile + 1;
+  if (hi <= lo) return lead + 1;
+  return lead + (hi - 1) / tile - lo / tile + 1;
 }
 
 // share of each CTA when `total` tiles are cut into at most `grid` equal runs of at least `least`
@@ -73,9 +74,10 @@ MONO_HD unsigned share_of(unsigned total, unsigned grid, unsigned least) {
   return u > least ? u : least;
 }
 
-// Partial results of an item (tiles [base, base + n) of the line): CTA c keeps
-// at most two unfinished items, the one its run begins in (slot 2c) and the
-// one that begins inside its run and goes on behind it (slot 2c + 1).
+// Partial results of an item (tiles [base, base + n) of the line, its start not
+// among them): CTA c keeps at most two unfinished items, the one its run begins
+// in (slot 2c) and the one that begins inside its run and goes on behind it
+// (slot 2c + 1).
 MONO_HD unsigned part_slot(unsigned c, unsigned base, unsigned share) {
   return 2u * c + (base > c * share ? 1u : 0u);
 }

@@ -51,6 +51,8 @@ struct OnDevice {
   }
 };
 
+constexpr size_t kSmemMax = 227 * 1024;   // of a CTA
+
 size_t elem(int dtype) { return dtype == MONO_BF16 ? 2 : 4; }
 
 int check_device(int device, std::string* why, int* sms) {
@@ -225,7 +227,7 @@ extern "C" int mono_rope_apply(const mono_rope* rope, int tokens, int heads, int
 struct mono_attn_plan_s {
   mono_attn_config cfg{};
   int page_shift = 0, sms = 0;
-  int grid[2] = {0, 0};   // CTAs of an attend launch with 8 rows a warp, and with 16
+  int grid[2][2] = {};   // CTAs of an attend launch with 8 rows a warp, and with 16; narrow and wide
   float* part_o = nullptr;
   float2* part_ml = nullptr;
   unsigned int* arrived = nullptr;
@@ -252,25 +254,51 @@ RowPlan plan_rows(int head_dim, int rows) {
   return r;
 }
 
+// A launch is narrow, CTAs of 4 warps with items of their own, or wide, one CTA
+// an SM, whose warps share an item.
+struct Launch {
+  RowPlan rows;
+  bool wide;
+  int warps(int head_dim) const { return wide ? attend_wide_warps(head_dim, rows.nt) : 4; }
+  // tokens of a round
+  int round(int head_dim) const {
+    return (head_dim == 256 ? 16 : head_dim == 64 && rows.nt == 1 ? 64 : 32) * (warps(head_dim) / rows.wr);
+  }
+};
+
+constexpr unsigned kLeastRounds = 1;   // of an attend CTA
+constexpr unsigned kLeadRounds = 2;    // that an item's start takes
+
 using AttendFn = void (*)(AttendParams);
 struct AttendKernel {
   AttendFn fn;
   size_t (*smem)(int, int);
 };
 template <int D, int NT, bool F32>
-AttendKernel attend_of() {
-  return {&attend_kernel<D, NT, F32>, &AttendShape<D, NT, F32>::smem};
+AttendKernel attend_pick(bool wide) {
+  constexpr int W = attend_wide_warps(D, NT);
+  if (wide) return {&attend_kernel<D, NT, F32, W>, &AttendShape<D, NT, F32, W>::smem};
+  return {&attend_kernel<D, NT, F32, 4>, &AttendShape<D, NT, F32, 4>::smem};
 }
-AttendKernel attend_for(int head_dim, int nt, bool f32) {
-  if (head_dim == 64) {
-    if (nt == 1) return f32 ? attend_of<64, 1, true>() : attend_of<64, 1, false>();
-    return f32 ? attend_of<64, 2, true>() : attend_of<64, 2, false>();
-  }
-  if (head_dim == 128) {
-    if (nt == 1) return f32 ? attend_of<128, 1, true>() : attend_of<128, 1, false>();
-    return f32 ? attend_of<128, 2, true>() : attend_of<128, 2, false>();
-  }
-  return f32 ? attend_of<256, 1, true>() : attend_of<256, 1, false>();
+template <bool F32>
+AttendKernel attend_of(int head_dim, int nt, bool wide) {
+  if (head_dim == 64) return nt == 1 ? attend_pick<64, 1, F32>(wide) : attend_pick<64, 2, F32>(wide);
+  if (head_dim == 128) return nt == 1 ? attend_pick<128, 1, F32>(wide) : attend_pick<128, 2, F32>(wide);
+  return attend_pick<256, 1, F32>(wide);
+}
+AttendKernel attend_for(int head_dim, bool f32, const Launch& l) {
+  return f32 ? attend_of<true>(head_dim, l.rows.nt, l.wide) : attend_of<false>(head_dim, l.rows.nt, l.wide);
+}
+
+// Wide up to one item (sequence, key head, row block) an SM: the parts of an
+// item to join are a third as many, and its phases have an SM's warps.  With
+// more items narrow CTAs run theirs side by side.  Heads 40 / 8 of 128, us
+// wide and narrow: 1 x 16000 tokens 20.0 and 29.2, 8 x 2000 18.9 and 22.9,
+// 8 x 4000 28.1 and 28.0, 64 x 200 28.8 and 22.1, 64 x 1000 54.6 and 39.3.
+// And where a sequence may be longer than a narrow CTA's round: at one token
+// 8.1 and 6.4.
+bool attend_wide(int64_t items, int sms, int64_t tokens, int narrow_round) {
+  return items <= sms && tokens > narrow_round;
 }
 
 using AppendFn = void (*)(AppendParams);
@@ -329,8 +357,8 @@ extern "C" int mono_attn_plan(const mono_attn_config* c, mono_attn_plan_t** out)
     if (why.empty()) {
       need((int64_t)c->max_pages * c->page_size < (1ll << 31) - 65536, "max_pages x page_size must stay below 2^31 - 65536");
       const RowPlan r = plan_rows(c->head_dim, c->max_new * (c->q_heads / c->kv_heads));
-      const int tile = c->head_dim == 64 ? 64 : c->head_dim == 128 ? 32 : 16;
-      const double tiles = (double)c->max_seqs * c->kv_heads * r.blocks * ((double)c->max_pages * c->page_size / tile + 2);
+      const double tiles = (double)c->max_seqs * c->kv_heads * r.blocks *
+                           ((double)c->max_pages * c->page_size / Launch{r, false}.round(c->head_dim) + 2 + kLeadRounds);
       need(tiles < 2147483648.0, "max_seqs x kv_heads x max_pages x page_size too large for the 32-bit work partition");
     }
     int sms = 0;
@@ -349,15 +377,16 @@ extern "C" int mono_attn_plan(const mono_attn_config* c, mono_attn_plan_t** out)
     size_t rows_max = 0;   // grid x rows of a CTA
     const int group = c->q_heads / c->kv_heads;
     int blocks = 1;
-    for (int w = 1; w <= c->max_new && e == cudaSuccess; ++w) {
-      const RowPlan r = plan_rows(c->head_dim, w * group);
-      const AttendKernel k = attend_for(c->head_dim, r.nt, c->dtype == MONO_F32);
+    for (int i = 2; i < 2 * c->max_new + 2 && e == cudaSuccess; ++i) {
+      const Launch l{plan_rows(c->head_dim, i / 2 * group), i % 2 == 1};
+      const RowPlan& r = l.rows;
+      const AttendKernel k = attend_for(c->head_dim, c->dtype == MONO_F32, l);
       const size_t smem = k.smem(c->max_seqs, r.wr);
       int occ = 0;
-      e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
-      if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k.fn, kAttendThreads, smem);
+      e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax);
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k.fn, 32 * l.warps(c->head_dim), smem);
       if (e == cudaSuccess && occ < 1) e = cudaErrorInvalidConfiguration;
-      int& g = p->grid[r.nt - 1];
+      int& g = p->grid[r.nt - 1][l.wide];
       g = g ? std::min(g, occ * p->sms) : occ * p->sms;
       rows_max = std::max(rows_max, (size_t)occ * p->sms * r.wr * 8 * r.nt);
       blocks = std::max(blocks, r.blocks);
@@ -476,8 +505,11 @@ extern "C" int mono_attn_attend(mono_attn_plan_t* p, const mono_kv_cache* c, con
     if (self_overlap(os, count, 3, p->cfg.head_dim)) return fail(MONO_ERR_INVALID_ARG, "attend: rows of out overlap");
     OnDevice on(p->cfg.device);
     const int group = p->cfg.q_heads / p->cfg.kv_heads;
+    const int64_t tokens = (int64_t)p->cfg.max_pages * p->cfg.page_size;
     const RowPlan r = plan_rows(p->cfg.head_dim, s->width * group);
-    const AttendKernel k = attend_for(p->cfg.head_dim, r.nt, p->cfg.dtype == MONO_F32);
+    const Launch l{r, attend_wide((int64_t)s->seqs * p->cfg.kv_heads * r.blocks, p->sms, tokens,
+                                   Launch{r, false}.round(p->cfg.head_dim))};
+    const AttendKernel k = attend_for(p->cfg.head_dim, p->cfg.dtype == MONO_F32, l);
     AttendParams a{};
     a.k = (const uint8_t*)c->k;
     a.v = (const uint8_t*)c->v;
@@ -506,9 +538,15 @@ extern "C" int mono_attn_attend(mono_attn_plan_t* p, const mono_kv_cache* c, con
     a.window = p->cfg.window;
     a.wr = r.wr;
     a.row_blocks = r.blocks;
-    a.least = 4 / r.wr;
+    a.least = kLeastRounds;
+    a.lead = kLeadRounds;
+    a.q_vec = aligned(q->p, 4 * el) && q->seq % 4 == 0 && q->token % 4 == 0 && q->head % 4 == 0;
+    a.o_vec = aligned(out->p, 4 * el) && out->seq % 4 == 0 && out->token % 4 == 0 && out->head % 4 == 0;
     a.scale_log2 = p->cfg.scale * 1.4426950408889634f;
-    k.fn<<<p->grid[r.nt - 1], kAttendThreads, k.smem(s->seqs, r.wr), (cudaStream_t)stream>>>(a);
+    // no more CTAs than the call can have rounds
+    const int64_t rounds = (tokens / l.round(p->cfg.head_dim) + 2 + kLeadRounds) * s->seqs * p->cfg.kv_heads * r.blocks;
+    const int grid = (int)std::min<int64_t>(p->grid[r.nt - 1][l.wide], rounds);
+    k.fn<<<grid, 32 * l.warps(p->cfg.head_dim), k.smem(s->seqs, r.wr), (cudaStream_t)stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? (int)MONO_OK : cuda_fail(e, "attend");
   });
@@ -534,7 +572,7 @@ extern "C" int mono_attn_query_error(mono_attn_plan_t* p, mono_attn_status* st) 
 
 extern "C" int mono_attn_get_info(const mono_attn_plan_t* p, mono_attn_info* info) {
   if (!p || !info) return MONO_ERR_INVALID_ARG;
-  info->grid = std::max(p->grid[0], p->grid[1]);
+  info->grid = std::max(std::max(p->grid[0][0], p->grid[0][1]), std::max(p->grid[1][0], p->grid[1][1]));
   info->scratch_bytes = p->scratch;
   return MONO_OK;
 }
@@ -574,8 +612,6 @@ size_t proj_smem_of(bool f32, int sc, bool zp, int rows, int kb) {
 }
 
 constexpr double kProjSumCost = 4, kProjPushCost = 7;   // of an output block's sums, in blocks of a warp
-constexpr size_t kProjSmemMax = 227 * 1024;
-
 }  // namespace
 
 extern "C" void mono_proj_destroy(mono_proj_plan_t* p) {
@@ -610,7 +646,7 @@ extern "C" int mono_proj_plan(const mono_proj_config* c, mono_proj_plan_t** out)
     const int kblocks = c->n_in / 32;
     const int sc = mx ? kScaleE8m0 : c->scale_dtype == MONO_F32 ? kScaleF32 : kScaleBf16;
     int limit = 1;   // blocks of a CTA that fit its shared memory
-    while (why.empty() && proj_smem_of(f32, sc, c->zeros != 0, 8, limit + 1) <= kProjSmemMax) ++limit;
+    while (why.empty() && proj_smem_of(f32, sc, c->zeros != 0, 8, limit + 1) <= kSmemMax) ++limit;
     need((kblocks + 7) / 8 <= limit, "n_in too large: " + std::to_string(limit * 8 * 32) + " at most for this dtype");
     int sms = 0;
     const int rc = check_device(c->device, &why, &sms);
@@ -644,7 +680,7 @@ extern "C" int mono_proj_plan(const mono_proj_config* c, mono_proj_plan_t** out)
     if (e == cudaSuccess && mx) e = dalloc(&p->special, 4, &p->packed);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(proj_for(f32, p->sc, c->zeros != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)kProjSmemMax);
+                               (int)kSmemMax);
     if (e != cudaSuccess) {
       cudaGetLastError();
       mono_proj_destroy(p);

@@ -118,16 +118,6 @@ __device__ __forceinline__ float e8m0_ends(float s) {   // 2^-127 and NaN
   return b == 0u ? __uint_as_float(0x00400000u) : b == 0x7F800000u ? __uint_as_float(0x7FC00000u) : s;
 }
 
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <int SC, bool ZP>
 __host__ __device__ constexpr int proj_slot() {   // bytes of a block in a warp's ring: codes, scales, zeros
   return 1024 + 64 * ScaleRegs<SC>::kBytes + (ZP ? 64 : 0);

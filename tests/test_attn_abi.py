@@ -195,8 +195,8 @@ void view(int len, int n_new, int width, int cap, int* o) {
 }
 int hi(int len, int n_new, int width, int cap, int j) { return row_hi(view_seq(len, n_new, width, cap), j, cap); }
 int lo(int len, int n_new, int width, int cap, int j, int w) { return row_lo(view_seq(len, n_new, width, cap), j, w); }
-int tiles(int len, int n_new, int width, int cap, int w, int t) {
-  return seq_tiles(view_seq(len, n_new, width, cap), w, cap, t);
+int tiles(int len, int n_new, int width, int cap, int w, int t, int lead) {
+  return seq_tiles(view_seq(len, n_new, width, cap), w, cap, t, lead);
 }
 int ok(int page, int n) { return page_ok(page, n); }
 long long row(int page, int heads, int h, int p, int tok) { return code_row(page, heads, h, p, tok); }
@@ -237,9 +237,9 @@ def test_rows_of_a_sequence(idx):
     top = 2 ** 31 - 1
     assert _view(idx, top, 8, 8, 1024)[1] == top - 8
     assert idx.hi(top, 8, 8, 1024, 7) == 1024 and idx.lo(top, 8, 8, 1024, 7, 5) == top - 5
-    assert idx.tiles(top, 8, 8, 1024, 5, 32) == 1              # nothing seen: one tile, so that rows are written
+    assert idx.tiles(top, 8, 8, 1024, 5, 32, 0) == 1              # nothing seen: one tile, so that rows are written
     assert [idx.hi(2, 4, 4, 64, j) for j in range(4)] == [-1, 0, 1, 2]
-    assert idx.tiles(0, 1, 1, 64, 0, 16) == 1 and idx.tiles(64, 0, 1, 64, 0, 16) == 0
+    assert idx.tiles(0, 1, 1, 64, 0, 16, 0) == 1 and idx.tiles(64, 0, 1, 64, 0, 16, 3) == 0
 
 
 def test_rows_see_what_the_definition_says(idx):
@@ -256,7 +256,8 @@ def test_rows_see_what_the_definition_says(idx):
             assert want == list(range(lo, max(lo, hi))), (length, n, j, w)
             assert hi <= cap and lo >= 0
             seen += want
-        count = idx.tiles(length, n, width, cap, w, t)
+        lead = rng.randint(0, 3)
+        count = idx.tiles(length, n, width, cap, w, t, lead) - lead
         first = idx.lo(length, n, width, cap, 0, w) // t
         assert set(x // t for x in seen) <= set(range(first, first + count)) and count >= 1
 
@@ -271,13 +272,14 @@ def test_equal_runs_cover_the_line_and_keep_their_slots(idx):
     own in each, below 2 x grid, and a CTA never uses a slot for two items."""
     rng = random.Random(2)
     for _ in range(400):
-        grid, least = rng.randint(1, 40), rng.choice([1, 2, 4])
+        grid, least, lead = rng.randint(1, 40), rng.choice([1, 2, 4]), rng.randint(0, 3)
         items = [rng.choice([1, 1, 2, rng.randint(1, 60)]) for _ in range(rng.randint(1, 40))]
-        total = sum(items)
+        total = sum(items) + lead * len(items)
         share = idx.share(total, grid, least)
         assert share >= least and share * grid >= total
         base, used = 0, set()
         for n in items:
+            base += lead
             first, last = base // share, (base + n - 1) // share
             assert last < grid
             if first != last:
