@@ -267,7 +267,7 @@ struct Launch {
 };
 
 constexpr unsigned kLeastRounds = 1;   // of an attend CTA
-constexpr unsigned kLeadRounds = 2;    // that an item's start takes
+constexpr unsigned kLeadRounds = 3;    // that an item's start takes
 
 using AttendFn = void (*)(AttendParams);
 struct AttendKernel {

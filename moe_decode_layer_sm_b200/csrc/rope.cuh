@@ -56,60 +56,82 @@ struct RopeParams {
 constexpr int kRopeThreads = 256;
 
 // One CTA: one token, heads_per_cta heads.  The angles are computed once for
-// the token and shared by its heads.  A thread owns whole pairs (both 16-byte
-// halves of a half-layout pair block), so x may be rotated in place.
+// the token and shared by its heads, while the first kAhead units of each
+// thread are on their way.  A thread owns whole pairs (both vectors of a
+// half-layout pair block), so x may be rotated in place.  Bound by memory: one
+// read and one write of every value (not in place: of the unrotated ones too).
 // VEC = 16 bytes of T where layout and alignment allow, else 1.
 template <typename T, int VEC, bool IL>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ __align__(16) float cs[128], sn[128];
   const int tok = blockIdx.x;
   const int pos = __ldg(p.pos + tok);
-  if (pos < 0) return;
   const int half = p.rope.rot_dim >> 1, off = p.rope.offset, rot = p.rope.rot_dim;
-  for (int i = threadIdx.x; i < half; i += kRopeThreads) rope_cs(p.rope, i, pos, p.transpose, &cs[i], &sn[i]);
-  __syncthreads();
-  const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(h0 + p.heads_per_cta, p.heads);
-  const T* x = reinterpret_cast<const T*>(p.x) + (long long)tok * p.x_token;
-  T* o = reinterpret_cast<T*>(p.out) + (long long)tok * p.o_token;
+  const int h0 = blockIdx.y * p.heads_per_cta, heads = min(p.heads_per_cta, p.heads - h0);
+  const T* x = reinterpret_cast<const T*>(p.x) + (long long)tok * p.x_token + (long long)h0 * p.x_head;
+  T* o = reinterpret_cast<T*>(p.out) + (long long)tok * p.o_token + (long long)h0 * p.o_head;
   // units of a head: rotated ones, then (not in place) the dimensions to copy
   constexpr int kPairs = IL ? (VEC > 1 ? VEC / 2 : 1) : VEC;   // pairs a rotated unit holds
+  constexpr bool kOne = IL && VEC > 1;                         // a rotated unit is one vector, not two
+  constexpr int kAhead = kOne ? 4 : 2;                         // units that a thread has in flight
   const int nrot = half / kPairs;
   const int ncopy = p.in_place ? 0 : (p.head_dim - rot) / VEC;
-  const int units = nrot + ncopy, total = units * (h1 - h0);
+  const int units = nrot + ncopy;
+  const int step_h = kRopeThreads / units, step_u = kRopeThreads - step_h * units;
+  int h = threadIdx.x / units, u = threadIdx.x - h * units;
   using V = Vec<T, VEC>;
-  for (int idx = threadIdx.x; idx < total; idx += kRopeThreads) {
-    const int h = h0 + idx / units, u = idx % units;
-    const T* xh = x + (long long)h * p.x_head;
-    T* oh = o + (long long)h * p.o_head;
-    if (u >= nrot) {
-      int d = (u - nrot) * VEC;
-      if (d >= off) d += rot;
-      *reinterpret_cast<V*>(oh + d) = *reinterpret_cast<const V*>(xh + d);
-    } else if (IL && VEC > 1) {
-      const int d = off + u * VEC;
-      V a = *reinterpret_cast<const V*>(xh + d);
+  bool first = true;
+  // every thread meets the barrier below, also one without a unit
+  while (first || h < heads) {
+    V a[kAhead], b[kAhead];
+    int at_h[kAhead], at_u[kAhead];
 #pragma unroll
-      for (int i = 0; i < VEC / 2; ++i) {
-        const float c = cs[u * kPairs + i], s = sn[u * kPairs + i];
-        const float x1 = to_f(a.v[2 * i]), x2 = to_f(a.v[(2 * i + 1) % VEC]);
-        a.v[2 * i] = from_f<T>(c * x1 - s * x2);
-        a.v[(2 * i + 1) % VEC] = from_f<T>(s * x1 + c * x2);
+    for (int k = 0; k < kAhead; ++k) {
+      at_h[k] = h, at_u[k] = u;
+      h += step_h, u += step_u;
+      if (u >= units) u -= units, ++h;
+      if (at_h[k] < heads) {
+        const T* xh = x + (long long)at_h[k] * p.x_head;
+        const int v = at_u[k];
+        if (v >= nrot) {
+          const int d = (v - nrot) * VEC;
+          a[k] = *reinterpret_cast<const V*>(xh + (d >= off ? d + rot : d));
+        } else {
+          const int d = off + v * (kOne ? VEC : IL ? 2 : kPairs);
+          a[k] = *reinterpret_cast<const V*>(xh + d);
+          if (!kOne) b[k] = *reinterpret_cast<const V*>(xh + (IL ? d + 1 : d + half));
+        }
       }
-      *reinterpret_cast<V*>(oh + d) = a;
-    } else {
-      const int i0 = u * kPairs;
-      const int da = IL ? off + 2 * i0 : off + i0, db = IL ? da + 1 : da + half;
-      V a = *reinterpret_cast<const V*>(xh + da), b = *reinterpret_cast<const V*>(xh + db);
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float c = cs[i0 + i], s = sn[i0 + i];
-        const float x1 = to_f(a.v[i]), x2 = to_f(b.v[i]);
-        a.v[i] = from_f<T>(c * x1 - s * x2);
-        b.v[i] = from_f<T>(s * x1 + c * x2);
-      }
-      *reinterpret_cast<V*>(oh + da) = a;
-      *reinterpret_cast<V*>(oh + db) = b;
     }
+    if (first) {
+      first = false;
+      for (int i = threadIdx.x; i < half; i += kRopeThreads) rope_cs(p.rope, i, pos, p.transpose, &cs[i], &sn[i]);
+      __syncthreads();
+      if (pos < 0) return;   // padding
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (at_h[k] < heads) {
+        T* oh = o + (long long)at_h[k] * p.o_head;
+        const int v = at_u[k];
+        if (v >= nrot) {
+          const int d = (v - nrot) * VEC;
+          *reinterpret_cast<V*>(oh + (d >= off ? d + rot : d)) = a[k];
+          continue;
+        }
+        const int d = off + v * (kOne ? VEC : IL ? 2 : kPairs), i0 = v * kPairs;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          const float c = cs[i0 + i], s = sn[i0 + i];
+          T& t1 = a[k].v[kOne ? 2 * i : i];
+          T& t2 = kOne ? a[k].v[(2 * i + 1) % VEC] : b[k].v[i % VEC];
+          const float x1 = to_f(t1), x2 = to_f(t2);
+          t1 = from_f<T>(c * x1 - s * x2);
+          t2 = from_f<T>(s * x1 + c * x2);
+        }
+        *reinterpret_cast<V*>(oh + d) = a[k];
+        if (!kOne) *reinterpret_cast<V*>(oh + (IL ? d + 1 : d + half)) = b[k];
+      }
   }
 }
 
