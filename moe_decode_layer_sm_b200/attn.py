@@ -235,18 +235,14 @@ class AttnPlan:
         self.q_heads, self.kv_heads, self.head_dim, self.max_pages = q_heads, kv_heads, head_dim, max_pages
         self._append, self._attend = self._lib.mono_attn_append, self._lib.mono_attn_attend
 
-    def _ok(self, cache, x, heads, y, lens, table, n_new):
-        """Whether a call's tensors are what they must be: x and y rows of `heads`
-        heads, one of each sequence's entries for each row of x."""
-        n, dev = x.shape[0], self.device
-        return (x.dtype is self.dtype and y.dtype is self.dtype and x.get_device() == dev and y.get_device() == dev
-                and x.dim() == 4 and x.shape[2] == heads and x.shape[3] == self.head_dim and y.shape == x.shape
-                and x.stride(3) == 1 and y.stride(3) == 1 and cache.shape == self.shape and cache.device == dev
-                and lens.dtype is torch.int32 and lens.shape == (n,) and lens.get_device() == dev
-                and lens.is_contiguous() and table.dtype is torch.int32 and table.shape == (n, self.max_pages)
-                and table.get_device() == dev and table.is_contiguous()
-                and (n_new is None or (n_new.dtype is torch.int32 and n_new.shape == (n,)
-                                       and n_new.get_device() == dev and n_new.is_contiguous())))
+    def _seqs_ok(self, cache, n, lens, table, n_new):
+        """Whether the cache and the entries of a call's n sequences are what they must be."""
+        dev, i32 = self.device, torch.int32
+        return (cache.shape == self.shape and cache.device == dev and lens.dtype is i32 and lens.shape == (n,)
+                and lens.get_device() == dev and lens.is_contiguous() and table.dtype is i32
+                and table.shape == (n, self.max_pages) and table.get_device() == dev and table.is_contiguous()
+                and (n_new is None or (n_new.dtype is i32 and n_new.shape == (n,) and n_new.get_device() == dev
+                                       and n_new.is_contiguous())))
 
     def _refuse(self, who, names, cache, x, heads, y, lens, table, n_new):
         why, d = [], self.device
@@ -270,22 +266,27 @@ class AttnPlan:
         if n_new is not None and (n_new.dtype != torch.int32 or tuple(n_new.shape) != (n,) or n_new.get_device() != d
                                   or not n_new.is_contiguous()):
             why.append("n_new must be contiguous int32 [seqs] on the plan's device")
-        _refuse(who, why)
+        _refuse(who, why or ["wrong arguments"])
 
     def append(self, cache, k, v, lens, table, rope=None, n_new=None, stream=None):
         """mono_attn_append: k, v [seqs][width][kv_heads][head_dim] (strides free)
         into the pages of `table` [seqs][max_pages]; lens [seqs] counts the new
         tokens, n_new [seqs] says how many of the rows are new (None: all).
         rope: the keys are rotated to their positions on the way."""
-        if k.dim() != 4 or not self._ok(cache, k, self.kv_heads, v, lens, table, n_new):
+        shape, dtype, dev = k.shape, self.dtype, self.device
+        if len(shape) != 4 or v.shape != shape:
             self._refuse("append", ("k", "v"), cache, k, self.kv_heads, v, lens, table, n_new)
-        n, width, _, _ = k.shape
-        ks, kt, kh, _ = k.stride()
-        vs, vt, vh, _ = v.stride()
+        n, width, heads, head_dim = shape
+        ks, kt, kh, kd = k.stride()
+        vs, vt, vh, vd = v.stride()
+        if not (heads == self.kv_heads and head_dim == self.head_dim and kd == 1 and vd == 1 and k.dtype is dtype
+                and v.dtype is dtype and k.get_device() == dev and v.get_device() == dev
+                and self._seqs_ok(cache, n, lens, table, n_new)):
+            self._refuse("append", ("k", "v"), cache, k, self.kv_heads, v, lens, table, n_new)
         rc = self._append(self.handle, cache._at,
                           _seqs(n, width, lens.data_ptr(), 0 if n_new is None else n_new.data_ptr(), table.data_ptr()),
                           _rows(k.data_ptr(), ks, kt, kh), _rows(v.data_ptr(), vs, vt, vh),
-                          None if rope is None else rope._at, _stream_of(self.device, stream))
+                          None if rope is None else rope._at, _stream_of(dev, stream))
         if rc:
             _check(rc)
 
@@ -293,18 +294,23 @@ class AttnPlan:
         """mono_attn_attend: out [seqs][width][q_heads][head_dim] of q (rotated; the
         same shape, strides free) over the cached tokens that each row sees.  lse:
         fp32 [seqs][width][q_heads], the log of the sum of exponentials.  Returns out."""
-        if q.dim() != 4 or not self._ok(cache, q, self.q_heads, out, lens, table, n_new):
+        shape, dtype, dev = q.shape, self.dtype, self.device
+        if len(shape) != 4 or out.shape != shape:
             self._refuse("attend", ("q", "out"), cache, q, self.q_heads, out, lens, table, n_new)
-        n, width, _, _ = q.shape
-        if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous()
-                                or lse.get_device() != self.device):
+        n, width, heads, head_dim = shape
+        qs, qt, qh, qd = q.stride()
+        os, ot, oh, od = out.stride()
+        if not (heads == self.q_heads and head_dim == self.head_dim and qd == 1 and od == 1 and q.dtype is dtype
+                and out.dtype is dtype and q.get_device() == dev and out.get_device() == dev
+                and self._seqs_ok(cache, n, lens, table, n_new)):
+            self._refuse("attend", ("q", "out"), cache, q, self.q_heads, out, lens, table, n_new)
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:3] or not lse.is_contiguous()
+                                or lse.get_device() != dev):
             raise ValueError("attend: lse must be contiguous fp32 [seqs][width][q_heads] on the plan's device")
-        qs, qt, qh, _ = q.stride()
-        os, ot, oh, _ = out.stride()
         rc = self._attend(self.handle, cache._at,
                           _seqs(n, width, lens.data_ptr(), 0 if n_new is None else n_new.data_ptr(), table.data_ptr()),
                           _rows(q.data_ptr(), qs, qt, qh), _rows(out.data_ptr(), os, ot, oh),
-                          None if lse is None else lse.data_ptr(), _stream_of(self.device, stream))
+                          None if lse is None else lse.data_ptr(), _stream_of(dev, stream))
         if rc:
             _check(rc)
         return out
@@ -380,13 +386,15 @@ class Projection:
 
     def step(self, x, y, stream=None):
         """y [rows][n_out] = x [rows][n_in] W^T, up to 8 rows, row strides free.  Returns y."""
-        dev = self.device
-        if not (x.dtype is self.dtype and y.dtype is self.dtype and x.get_device() == dev and y.get_device() == dev
-                and x.dim() == 2 and x.shape[1] == self.n_in and y.shape == (x.shape[0], self.n_out)
-                and x.stride(1) == 1 and (y.stride(1) == 1 or self.n_out == 1)):
+        shape, dtype, dev = x.shape, self.dtype, self.device
+        if len(shape) != 2 or shape[1] != self.n_in or y.shape != (shape[0], self.n_out):
             self._refuse_step(x, y)
-        rc = self._step(self.handle, x.shape[0], x.data_ptr(), x.stride(0), y.data_ptr(), y.stride(0),
-                        _stream_of(dev, stream))
+        xr, xd = x.stride()
+        yr, yd = y.stride()
+        if not (xd == 1 and (yd == 1 or self.n_out == 1) and x.dtype is dtype and y.dtype is dtype
+                and x.get_device() == dev and y.get_device() == dev):
+            self._refuse_step(x, y)
+        rc = self._step(self.handle, shape[0], x.data_ptr(), xr, y.data_ptr(), yr, _stream_of(dev, stream))
         if rc:
             _check(rc)
         return y
@@ -401,7 +409,7 @@ class Projection:
             why.append(f"x and y must be {self.dtype}")
         if x.get_device() != self.device or y.get_device() != self.device:
             why.append("x and y must be on the plan's device")
-        _refuse("step", why)
+        _refuse("step", why or ["wrong arguments"])
 
     def info(self):
         inf = ProjInfo()

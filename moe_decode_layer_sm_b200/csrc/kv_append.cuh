@@ -1,6 +1,8 @@
 // The append to the paged 8-bit cache: rotate the new keys, find each touched
 // page's scale, encode, and re-encode a page's older codes where its scale grows.
 #pragma once
+#include <type_traits>
+
 #include "kv_index.h"
 #include "rope.cuh"
 
@@ -32,8 +34,21 @@ struct AppendParams {
   mono_rope rope;
 };
 
+// all but the N newest groups of asynchronous copies have arrived
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 constexpr float kFp8Max = 448.0f;
 constexpr int kAppendThreads = 512;   // of a CTA at most
+__host__ __device__ constexpr int append_threads(int units) { return units == 4 ? kAppendThreads : 256; }
+
+__device__ __forceinline__ float rcp_approx(float x) {   // to one unit in the last place
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // A float whose nearest e4m3 value is that of q: truncated, with its last bit
 // set if anything was cut off, so that rounding twice cannot pass a border.
@@ -51,14 +66,16 @@ __device__ __forceinline__ bool fp8_near_border(float q) {
   return ((__float_as_uint(m) + 0x80008u) & 0xFFFF0u) == 0u;
 }
 
-// q = x / s near a border: on the side of it where the exact quotient lies, or
-// on it.  The border has 5 bits, so the sign of x - border x s is exact.
-__device__ __forceinline__ float fp8_settle(float q, float x, float s) {
-  const float low = fabsf(q) < 0.015625f ? 0.015625f : 0.f;
+// q, an approximation of x / s (finite, s a normal number well above the
+// smallest), moved next to the border between its two codes, to the side on
+// which the exact quotient lies, or onto it.  The border has 5 bits, so the
+// sign of x - border x s is exact.  A q that lies beyond a code ends next to
+// that code's other border, on the side of the code.  low: 2^-6 where |q| is
+// below it (codes are as far apart there as above), else 0.
+__device__ __forceinline__ float fp8_place(float q, float x, float s, float low) {
   const float b = __uint_as_float((__float_as_uint(fabsf(q) + low) & 0xFFF00000u) | 0x80000u) - low;
-  const float r = fmaf(-b, s, fabsf(x));
-  const uint32_t y = __float_as_uint(b) + (r > 0.f ? 1u : r < 0.f ? 0xFFFFFFFFu : 0u);
-  return __uint_as_float(y | (__float_as_uint(q) & 0x80000000u));
+  const int r = __float_as_int(fmaf(-b, s, fabsf(x)));
+  return __uint_as_float((__float_as_uint(b) + min(max(r, -1), 1)) | (__float_as_uint(q) & 0x80000000u));
 }
 
 __device__ __forceinline__ uint16_t fp8_pair(float lo, float hi) {
@@ -72,25 +89,6 @@ __device__ __forceinline__ uint2 fp8_pack8(const float* q) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = fp8_pair(q[2 * i], q[2 * i + 1]);
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
-}
-
-// eight values from a row, by one or two 16-byte loads where that is allowed
-template <typename T>
-__device__ __forceinline__ Vec<T, 8> load8(const T* p, bool wide) {
-  Vec<T, 8> v;
-  if (wide) {
-    constexpr int N = 16 / sizeof(T);
-#pragma unroll
-    for (int i = 0; i < 8 / N; ++i) {
-      const Vec<T, N> a = reinterpret_cast<const Vec<T, N>*>(p)[i];
-#pragma unroll
-      for (int j = 0; j < N; ++j) v.v[i * N + j] = a.v[j];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v.v[i] = p[i];
-  }
-  return v;
 }
 
 __device__ __forceinline__ double2 turn_by(double2 a, double2 b) {   // angles added
@@ -149,11 +147,23 @@ __device__ __noinline__ double finite_max8(const Turns& turns, bool rotate, cons
   return most;
 }
 
-// shared memory of `most` new tokens in a page
-__host__ __device__ inline size_t append_smem(int most, int rot_dim) {
+// heads that a thread has in flight or in use, and their bytes in a CTA
+template <typename T, int U>
+__host__ __device__ constexpr int append_heads() {
+  return U == 4 ? 4 / (int)sizeof(T) : sizeof(T) == 2 ? 3 : 2;
+}
+template <typename T, int U>
+__host__ __device__ constexpr size_t append_ring(int threads) {
+  return (size_t)append_heads<T, U>() * U * 16 * sizeof(T) * threads;
+}
+
+// shared memory of the angles of `most` new tokens in a page
+__host__ __device__ inline size_t append_angles(int most, int rot_dim) {
   return (size_t)((most + 7) / 8 + (most < 8 ? most : 8)) * 8 * ((rot_dim / 2 + 7) / 8) * sizeof(double2);
 }
 
+// positive numbers order as their bits do
+__device__ __forceinline__ unsigned int warp_max(unsigned int v) { return __reduce_max_sync(0xFFFFFFFFu, v); }
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   const unsigned int hi = __reduce_max_sync(0xFFFFFFFFu, (unsigned int)(v >> 32));
   const unsigned int lo = __reduce_max_sync(0xFFFFFFFFu, (unsigned int)(v >> 32) == hi ? (unsigned int)v : 0u);
@@ -164,7 +174,7 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 // of k or of v.  grid (pages a sequence's new tokens can touch, 2 x head
 // groups, sequences).  A page's head is held in registers between the two
 // passes that its scale needs (largest magnitude, then the codes), so the
-// input is read once, the next head's while this one's is reduced.
+// input is read once, and the next heads' are on their way meanwhile.
 //
 // The rotation is done in binary64 and a code near a border is found from it
 // again, so codes and scales are those of the exact rotated values: a key's
@@ -176,8 +186,8 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 // U: units of 16 values that a thread holds of a page's head.  EACH: rotations
 // whose offset or halves no vector of eight respects.
 template <typename T, int U, bool EACH>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
-  extern __shared__ __align__(16) unsigned char smem_append[];   // near [8][slots], far [tokens / 8][slots]
+__global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kernel(const __grid_constant__ AppendParams p) {
+  extern __shared__ __align__(16) unsigned char smem_append[];   // the ring, near [8][slots], far [tokens / 8][slots]
   __shared__ unsigned long long red[2][kAppendThreads / 32];
   const int s = blockIdx.z, which = blockIdx.y & 1, hg = blockIdx.y >> 1;
   const int P = 1 << p.page_shift, D = p.head_dim, cap = p.max_pages << p.page_shift;
@@ -209,38 +219,59 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   const T* x0 = reinterpret_cast<const T*>(p.x[which]) + (long long)s * p.x_seq[which] +
                 (long long)(a - sv.first) * p.x_tok[which];
 
-  int tok[U], da[U], db[U], pair[U];   // token, the two vectors' places, kHalves: first pair or -1
+  // a unit's token, its first vector's place and the second's from there, its
+  // first pair (kHalves; -1: not rotated), and where the first vector is read
+  int tok[U], da[U], dx[U], pair[U];
   bool live[U];
+  const T* from[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int idx = threadIdx.x + u * blockDim.x, c = idx & ((1 << upt_log2) - 1);
     live[u] = idx < nunits;
     tok[u] = idx >> upt_log2;
-    da[u] = c * 16, db[u] = da[u] + 8, pair[u] = -1;
+    da[u] = c * 16, dx[u] = 8, pair[u] = -1;
     if (!EACH && mode == kHalves) {
       const int nh = half >> 3, j = 16 * (c - nh);
-      if (c < nh) pair[u] = c * 8, da[u] = off + c * 8, db[u] = da[u] + half;
-      else da[u] = j < off ? j : j + rot, db[u] = j + 8 < off ? j + 8 : j + 8 + rot;
+      if (c < nh) {
+        pair[u] = c * 8, da[u] = off + c * 8, dx[u] = half;
+      } else {
+        da[u] = j < off ? j : j + rot;
+        dx[u] = (j + 8 < off ? j + 8 : j + 8 + rot) - da[u];
+      }
     }
+    from[u] = x0 + (long long)h0 * p.x_head[which] + (long long)tok[u] * p.x_tok[which] + da[u];
   }
   auto row_of = [&](int h, int u) { return x0 + (long long)h * p.x_head[which] + (long long)tok[u] * p.x_tok[which]; };
-  Vec<T, 8> raw[U][2];
-  auto fetch = [&](int h) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (live[u]) {
-        const T* row = row_of(h, u);
-        raw[u][0] = load8(row + da[u], p.vec_ok);
-        raw[u][1] = load8(row + db[u], p.vec_ok);
-      }
+  // A thread's values of kHeads heads in shared memory, each asked for kHeads
+  // heads before it is used; a thread reads only what it copied.  Rows that
+  // 16-byte copies cannot take are read when they are needed.
+  constexpr int kHeads = append_heads<T, U>(), kVecs = sizeof(T) / 2;   // 16-byte pieces of eight values
+  auto place = [&](int head, int u, int v, int k) {
+    return ((((head % kHeads) * U + u) * 2 + v) * kVecs + k) * blockDim.x + threadIdx.x;
   };
-  constexpr bool kAhead = U * sizeof(T) <= 8;   // registers for the next head's values
-  if (kAhead) fetch(h0);
+  uint4* ring = reinterpret_cast<uint4*>(smem_append);
+  auto fetch = [&](int head) {
+    if (p.vec_ok && head < h1 - h0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (live[u]) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k)
+              cp_async16(ring + place(head, u, v, k), from[u] + v * dx[u] + k * (16 / (int)sizeof(T)));
+          from[u] += p.x_head[which];
+        }
+    }
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kHeads - 1; ++i) fetch(i);
 
   Turns turns{nullptr, nullptr, half, off, (half + 7) >> 3, p.rope.interleaved != 0};
   if (mode != kPlain) {
     const int n_far = (b - a + 7) >> 3, n_near = min(b - a, 8), slots = 8 * turns.step;
-    double2* near = reinterpret_cast<double2*>(smem_append);
+    double2* near = reinterpret_cast<double2*>(smem_append + append_ring<T, U>(blockDim.x));
     double2* far = near + n_near * slots;
     for (int i = threadIdx.x; i < 2 * half; i += blockDim.x) {
       const bool is_far = i < half;
@@ -266,129 +297,163 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   }
 
   int turn = 0;
-  for (int h = h0; h < h1; ++h) {
-    float* scale_at = p.scales[which] + (long long)page * p.kv_heads + h;
-    const float was = older > 0 ? *scale_at : 0.f;
-    if (!kAhead) fetch(h);
-    float val[U][16];
-    double amax = 0.0;
-    float top = 0.f;   // of the values that are not rotated
+  auto block_max = [&](auto v) {
+    decltype(v)* at = reinterpret_cast<decltype(v)*>(red[turn]);   // red has two places: the one after next
+    v = warp_max(v);                                               // writes here behind the next barrier
+    if ((threadIdx.x & 31) == 0) at[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = warp_max((threadIdx.x & 31) < (blockDim.x >> 5) ? at[threadIdx.x & 31] : decltype(v)(0));
+    turn ^= 1;
+    return v;
+  };
+  float* scale_at = p.scales[which] + (long long)page * p.kv_heads + h0;
+  uint8_t* dst = p.codes[which] + code_row(page, p.kv_heads, h0, P, 0) * D;
+  auto heads = [&](auto plain) {
+    constexpr bool PLAIN = decltype(plain)::value;   // nothing is rotated
+    for (int h = h0; h < h1; ++h, ++scale_at, dst += P * D) {
+      const float was = older > 0 ? *scale_at : 0.f;
+      fetch(h - h0 + kHeads - 1);
+      cp_async_wait<kHeads - 1>();
+      float val[U][16];
+      double amax = 0.0;
+      float top = 0.f;   // of the values that are not rotated
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (live[u]) {
-        if (!EACH && mode == kHalves && pair[u] >= 0) {
+      for (int u = 0; u < U; ++u)
+        if (live[u]) {
+          Vec<T, 8> raw[2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const double2 cs = turns.at(tok[u], pair[u] + i);
-            const double x1 = to_f(raw[u][0].v[i]), x2 = to_f(raw[u][1].v[i]);
-            const double y1 = cs.x * x1 - cs.y * x2, y2 = cs.y * x1 + cs.x * x2;
-            amax = fmax(amax, fabs(y1));   // NaN is left out
-            amax = fmax(amax, fabs(y2));
-            val[u][i] = (float)y1, val[u][8 + i] = (float)y2;
-          }
-        } else {
+          for (int v = 0; v < 2; ++v)
+            if (p.vec_ok) {
 #pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            const int d = v ? db[u] : da[u];
-            if (!EACH && mode == kInterleaved && d >= off && d < off + rot) {
-#pragma unroll
-              for (int i = 0; i < 8; i += 2) {
-                const double2 cs = turns.at(tok[u], (d - off + i) >> 1);
-                const double x1 = to_f(raw[u][v].v[i]), x2 = to_f(raw[u][v].v[i + 1]);
-                const double y1 = cs.x * x1 - cs.y * x2, y2 = cs.y * x1 + cs.x * x2;
-                amax = fmax(amax, fabs(y1));   // NaN is left out
-                amax = fmax(amax, fabs(y2));
-                val[u][8 * v + i] = (float)y1, val[u][8 * v + i + 1] = (float)y2;
-              }
+              for (int k = 0; k < kVecs; ++k)
+                reinterpret_cast<uint4*>(&raw[v])[k] = ring[place(h - h0, u, v, k)];
             } else {
+              const T* at = row_of(h, u) + da[u] + v * dx[u];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                float x = to_f(raw[u][v].v[i]);
-                if (EACH && mode == kEach && d + i >= off && d + i < off + rot) {
-                  const double y = turns.one(row_of(h, u), tok[u], d + i);
-                  amax = fmax(amax, fabs(y));
-                  x = (float)y;
-                } else {
-                  top = fmaxf(top, fabsf(x));
+              for (int i = 0; i < 8; ++i) raw[v].v[i] = at[i];
+            }
+          if (!PLAIN && !EACH && mode == kHalves && pair[u] >= 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const double2 cs = turns.at(tok[u], pair[u] + i);
+              const double x1 = to_f(raw[0].v[i]), x2 = to_f(raw[1].v[i]);
+              const double y1 = cs.x * x1 - cs.y * x2, y2 = cs.y * x1 + cs.x * x2;
+              amax = fmax(amax, fmax(fabs(y1), fabs(y2)));   // NaN is left out
+              val[u][i] = (float)y1, val[u][8 + i] = (float)y2;
+            }
+          } else {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const int d = da[u] + v * dx[u];
+              if (!PLAIN && !EACH && mode == kInterleaved && d >= off && d < off + rot) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                  const double2 cs = turns.at(tok[u], (d - off + i) >> 1);
+                  const double x1 = to_f(raw[v].v[i]), x2 = to_f(raw[v].v[i + 1]);
+                  const double y1 = cs.x * x1 - cs.y * x2, y2 = cs.y * x1 + cs.x * x2;
+                  amax = fmax(amax, fmax(fabs(y1), fabs(y2)));
+                  val[u][8 * v + i] = (float)y1, val[u][8 * v + i + 1] = (float)y2;
                 }
-                val[u][8 * v + i] = x;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  float x = to_f(raw[v].v[i]);
+                  if (!PLAIN && EACH && d + i >= off && d + i < off + rot) {
+                    const double y = turns.one(row_of(h, u), tok[u], d + i);
+                    amax = fmax(amax, fabs(y));
+                    x = (float)y;
+                  } else {
+                    top = fmaxf(top, fabsf(x));
+                  }
+                  val[u][8 * v + i] = x;
+                }
               }
             }
           }
         }
+      // the largest of the page's head
+      if (PLAIN) {
+        amax = __uint_as_float(block_max(__float_as_uint(top)));
+      } else {
+        amax = fmax(amax, (double)top);
+        amax = __longlong_as_double((long long)block_max((unsigned long long)__double_as_longlong(amax)));
       }
-    if (kAhead && h + 1 < h1) fetch(h + 1);
-    // the largest of the page's head; positive doubles order as their bits do
-    amax = fmax(amax, (double)top);
-    auto block_max = [&](unsigned long long v) {
-      v = warp_max(v);
-      if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = v;
-      __syncthreads();   // red has two places: the one after next writes here behind the next barrier
-      v = warp_max((threadIdx.x & 31) < (blockDim.x >> 5) ? red[turn][threadIdx.x & 31] : 0ull);
-      turn ^= 1;
-      return __longlong_as_double((long long)v);
-    };
-    amax = block_max((unsigned long long)__double_as_longlong(amax));
-    if (!(amax < 1e300)) {   // an infinity among them: once more, without
-      amax = 0.0;
+      const bool infinite = !(amax < 1e300);
+      if (infinite) {   // an infinity among them: once more, without
+        amax = 0.0;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (live[u]) {
+            amax = fmax(amax, finite_max8(turns, !PLAIN, row_of(h, u), tok[u], da[u]));
+            amax = fmax(amax, finite_max8(turns, !PLAIN, row_of(h, u), tok[u], da[u] + dx[u]));
+          }
+        amax = __longlong_as_double((long long)block_max((unsigned long long)__double_as_longlong(amax)));
+      }
+      // amax / 448, correctly rounded (one step from the product with the inverse), at least 2^-126
+      const float af = (float)amax, q0 = af * (1.f / kFp8Max);
+      float sc = fmaxf(PLAIN ? fmaf(fmaf(-q0, kFp8Max, af), 1.f / kFp8Max, q0) : (float)(amax * (1.0 / (double)kFp8Max)),
+                       1.175494351e-38f);
+      if (older > 0) sc = fmaxf(sc, was);
+      const float rs = rcp_approx(sc);
+      const bool exact = infinite || sc < 1e-27f;   // fp8_place does not hold
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (live[u]) {
-          amax = fmax(amax, finite_max8(turns, mode != kPlain, row_of(h, u), tok[u], da[u]));
-          amax = fmax(amax, finite_max8(turns, mode != kPlain, row_of(h, u), tok[u], db[u]));
-        }
-      amax = block_max((unsigned long long)__double_as_longlong(amax));
-    }
-    float sc = fmaxf((float)(amax / (double)kFp8Max), 1.175494351e-38f);
-    if (older > 0) sc = fmaxf(sc, was);
-    const float rs = __fdiv_rn(1.f, sc);
-    uint8_t* dst = p.codes[which] + code_row(page, p.kv_heads, h, P, 0) * D;
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (live[u]) {
+          for (int v = 0; v < 2; ++v) {
+            const int d = da[u] + v * dx[u];
+            uint8_t* to = dst + (older + tok[u]) * D + d;
+            const bool turned = !PLAIN && (EACH || (mode == kHalves ? pair[u] >= 0 : d >= off && d < off + rot));
+            unsigned int near = 0u;
+            float y[8];
+            bool small = false;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int d = v ? db[u] : da[u];
-          uint8_t* to = dst + (older + tok[u]) * D + d;
-          unsigned int near = 0u;
-          float y[8];
+            for (int i = 0; i < 8; ++i) {
+              y[i] = val[u][8 * v + i] * rs;
+              small |= fabsf(y[i]) < 0.015625f;
+            }
+            if (!turned && !exact) {   // the values as they came: bf16's meet borders often
+              if (small) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            y[i] = val[u][8 * v + i] * rs;
-            if (fp8_near_border(y[i])) near |= 1u << i;
-          }
-          // (bf16 values meet borders often: 0.3 % of them, half of a warp's vectors)
-          if (!EACH && near && !(mode == kHalves ? pair[u] >= 0 : mode == kInterleaved && d >= off && d < off + rot)) {
+                for (int i = 0; i < 8; ++i)
+                  y[i] = fp8_place(y[i], val[u][8 * v + i], sc, fabsf(y[i]) < 0.015625f ? 0.015625f : 0.f);
+              } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (near & (1u << i)) y[i] = fp8_settle(y[i], val[u][8 * v + i], sc);
-            near = 0u;
-          }
-          *reinterpret_cast<uint2*>(to) = fp8_pack8(y);
+                for (int i = 0; i < 8; ++i) y[i] = fp8_place(y[i], val[u][8 * v + i], sc, 0.f);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (fp8_near_border(y[i])) near |= 1u << i;
+            }
+            *reinterpret_cast<uint2*>(to) = fp8_pack8(y);
 #pragma unroll 1
-          for (; near; near &= near - 1) {
-            const int e = d + __ffs(near) - 1;
-            to[e - d] = exact_code(turns, mode != kPlain && e >= off && e < off + rot, row_of(h, u), tok[u], e, sc);
+            for (; near; near &= near - 1) {
+              const int e = d + __ffs(near) - 1;
+              to[e - d] = exact_code(turns, !PLAIN && e >= off && e < off + rot, row_of(h, u), tok[u], e, sc);
+            }
           }
         }
-      }
-    if (older > 0 && sc > was) {
-      const double ratio = (double)was / (double)sc;
-      for (int idx = threadIdx.x; idx < older << (upt_log2 + 1); idx += blockDim.x) {
-        uint2* at = reinterpret_cast<uint2*>(dst + idx * 8);
-        const uint2 w = *at;
-        float v[8];
+      if (older > 0 && sc > was) {
+        const double ratio = (double)was / (double)sc;
+        for (int idx = threadIdx.x; idx < older << (upt_log2 + 1); idx += blockDim.x) {
+          uint2* at = reinterpret_cast<uint2*>(dst + idx * 8);
+          const uint2 w = *at;
+          float v[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = e4m3x2_to_f2((uint16_t)((i < 2 ? w.x : w.y) >> (16 * (i & 1))));
-          v[2 * i] = fp8_sticky((double)f.x * ratio);
-          v[2 * i + 1] = fp8_sticky((double)f.y * ratio);
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = e4m3x2_to_f2((uint16_t)((i < 2 ? w.x : w.y) >> (16 * (i & 1))));
+            v[2 * i] = fp8_sticky((double)f.x * ratio);
+            v[2 * i + 1] = fp8_sticky((double)f.y * ratio);
+          }
+          *at = fp8_pack8(v);
         }
-        *at = fp8_pack8(v);
       }
+      if (threadIdx.x == 0) *scale_at = sc;
     }
-    if (threadIdx.x == 0) *scale_at = sc;
-  }
+  };
+  if (mode == kPlain) heads(std::true_type{});
+  else heads(std::false_type{});
 }
 
 }  // namespace mono

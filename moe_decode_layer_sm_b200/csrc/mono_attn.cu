@@ -302,13 +302,19 @@ bool attend_wide(int64_t items, int sms, int64_t tokens, int narrow_round) {
 }
 
 using AppendFn = void (*)(AppendParams);
-int append_units(int page_size, int head_dim) { return page_size * head_dim > 2 * 16 * kAppendThreads ? 4 : 2; }
-template <typename T>
-AppendFn append_pick(int units, bool each) {
-  if (units == 4) return each ? &append_kernel<T, 4, true> : &append_kernel<T, 4, false>;
-  return each ? &append_kernel<T, 2, true> : &append_kernel<T, 2, false>;
+struct AppendKernel {
+  AppendFn fn;
+  size_t (*ring)(int);
+};
+template <typename T, int U>
+AppendKernel append_pick(bool each) {
+  return {each ? &append_kernel<T, U, true> : &append_kernel<T, U, false>, &append_ring<T, U>};
 }
-AppendFn append_for(bool f32, int units, bool each) {
+template <typename T>
+AppendKernel append_pick(int units, bool each) {
+  return units == 4 ? append_pick<T, 4>(each) : units == 2 ? append_pick<T, 2>(each) : append_pick<T, 1>(each);
+}
+AppendKernel append_for(bool f32, int units, bool each) {
   return f32 ? append_pick<float>(units, each) : append_pick<__nv_bfloat16>(units, each);
 }
 
@@ -371,9 +377,9 @@ extern "C" int mono_attn_plan(const mono_attn_config* c, mono_attn_plan_t** out)
     while ((1 << p->page_shift) < c->page_size) ++p->page_shift;
     p->sms = sms;
     cudaError_t e = cudaSuccess;
-    for (int each = 0; each < 2 && e == cudaSuccess; ++each)
-      e = cudaFuncSetAttribute(append_for(c->dtype == MONO_F32, append_units(c->page_size, c->head_dim), each),
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, 56 * 1024);
+    for (int i = 0; i < 6 && e == cudaSuccess; ++i)
+      e = cudaFuncSetAttribute(append_for(c->dtype == MONO_F32, 1 << i / 2, i % 2).fn,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMax - 1024);
     size_t rows_max = 0;   // grid x rows of a CTA
     const int group = c->q_heads / c->kv_heads;
     int blocks = 1;
@@ -473,15 +479,17 @@ extern "C" int mono_attn_append(mono_attn_plan_t* p, const mono_kv_cache* c, con
     // heads share a CTA's angles once there are CTAs enough without them
     int hpc = 1;
     while (hpc < p->cfg.kv_heads && hpc < 8 &&
-           (int64_t)spans * s->seqs * 2 * ((p->cfg.kv_heads + 2 * hpc - 1) / (2 * hpc)) >= 4 * p->sms)
+           (int64_t)spans * s->seqs * 2 * ((p->cfg.kv_heads + 2 * hpc - 1) / (2 * hpc)) >= 8 * p->sms)
       hpc *= 2;
     a.heads_per_cta = hpc;
     const int groups = (p->cfg.kv_heads + hpc - 1) / hpc;
-    const int units = append_units(P, D), threads = std::max(64, P * D / (16 * units));
-    const size_t smem = rope ? append_smem(std::min(P, s->width), rope->rot_dim) : 0;
+    const int most = std::min(P, s->width), total = most * D / 16;   // new tokens of a page, units of 16 values
+    const int units = total <= append_threads(1) ? 1 : total <= 2 * append_threads(2) ? 2 : 4;
+    const int threads = std::max(128, (total / units + 31) / 32 * 32);   // (older codes may have to be taken along)
     const bool each = rope && ((rope->offset | (rope->interleaved ? rope->rot_dim : rope->rot_dim / 2)) & 7);
-    append_for(p->cfg.dtype == MONO_F32, units, each)<<<dim3(spans, 2 * groups, s->seqs), threads, smem,
-                                                        (cudaStream_t)stream>>>(a);
+    const AppendKernel kernel = append_for(p->cfg.dtype == MONO_F32, units, each);
+    const size_t smem = kernel.ring(threads) + (rope ? append_angles(most, rope->rot_dim) : 0);
+    kernel.fn<<<dim3(spans, 2 * groups, s->seqs), threads, smem, (cudaStream_t)stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? (int)MONO_OK : cuda_fail(e, "append");
   });
