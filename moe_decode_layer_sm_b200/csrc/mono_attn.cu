@@ -166,8 +166,9 @@ std::string rope_reasons(const mono_rope* r, int head_dim) {
 
 template <typename T, int VEC>
 void launch_rope(const RopeParams& p, dim3 grid, cudaStream_t st) {
-  if (p.rope.interleaved) rope_kernel<T, VEC, true><<<grid, kRopeThreads, 0, st>>>(p);
-  else rope_kernel<T, VEC, false><<<grid, kRopeThreads, 0, st>>>(p);
+  const size_t smem = (size_t)p.tokens_per_cta * (p.rope.rot_dim / 2) * sizeof(float2);
+  if (p.rope.interleaved) rope_kernel<T, VEC, true><<<grid, kRopeThreads, smem, st>>>(p);
+  else rope_kernel<T, VEC, false><<<grid, kRopeThreads, smem, st>>>(p);
 }
 
 }  // namespace
@@ -196,19 +197,25 @@ extern "C" int mono_rope_apply(const mono_rope* rope, int tokens, int heads, int
     } else if (meet(extent(x, el, xs, count, 2, head_dim), extent(out, el, os, count, 2, head_dim))) {
       return fail(MONO_ERR_INVALID_ARG, "rope_apply: x and out overlap");
     }
-    RopeParams p{*rope, x, out, pos, x_token, x_head, out_token, out_head, heads, head_dim, heads, transpose != 0,
-                 in_place};
-    // one CTA a token; few tokens: their heads in several CTAs, so that about two fit each SM
-    int parts = 1;
-    if (tokens < 296) parts = std::min(heads, (296 + tokens - 1) / tokens);
-    p.heads_per_cta = (heads + parts - 1) / parts;
-    const dim3 grid(tokens, (heads + p.heads_per_cta - 1) / p.heads_per_cta);
+    RopeParams p{*rope, x, out, pos, x_token, x_head, out_token, out_head, tokens, heads, head_dim, 1, heads,
+                 transpose != 0, in_place};
     // 16-byte vectors where every one of them is aligned and holds whole pairs of one kind
     const int vec = (int)(16 / el);
     const int unit = rope->interleaved ? rope->rot_dim : rope->rot_dim / 2;
     const bool wide = unit % vec == 0 && rope->offset % vec == 0 && head_dim % vec == 0 && aligned(x, 16) &&
                       aligned(out, 16) && x_token % vec == 0 && x_head % vec == 0 && out_token % vec == 0 &&
                       out_head % vec == 0;
+    // Ten vectors a thread: few heads bring more tokens into a CTA (16000 tokens
+    // of one head, bf16: 37 us with one each, 12 with 16), as long as there are
+    // four CTAs an SM; few tokens bring their heads into several CTAs.  8191 x 40
+    // heads, bf16, with 1, 4, 8 and 16 tokens a CTA: 48, 35, 32 and 36 us.
+    constexpr int kSms = 148;
+    const int64_t row = (int64_t)heads * head_dim / (wide ? vec : 1);
+    p.tokens_per_cta = (int)std::min<int64_t>({kRopeTokens, (2559 + row) / row, std::max(1, tokens / (4 * kSms))});
+    int parts = 1;
+    if (tokens < 2 * kSms) parts = std::min(heads, (2 * kSms + tokens - 1) / tokens);
+    p.heads_per_cta = (heads + parts - 1) / parts;
+    const dim3 grid((tokens + p.tokens_per_cta - 1) / p.tokens_per_cta, (heads + p.heads_per_cta - 1) / p.heads_per_cta);
     cudaStream_t st = (cudaStream_t)stream;
     if (dtype == MONO_BF16) {
       if (wide) launch_rope<__nv_bfloat16, 8>(p, grid, st);

@@ -50,48 +50,52 @@ struct RopeParams {
   void* out;
   const int* pos;
   long long x_token, x_head, o_token, o_head;
-  int heads, head_dim, heads_per_cta, transpose, in_place;
+  int tokens, heads, head_dim, tokens_per_cta, heads_per_cta, transpose, in_place;
 };
 
 constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 16;   // of a CTA at most
 
-// One CTA: one token, heads_per_cta heads.  The angles are computed once for
-// the token and shared by its heads, while the first kAhead units of each
+// One CTA: tokens_per_cta tokens, heads_per_cta heads.  A token's angles are
+// computed once and shared by its heads, while the first kAhead units of each
 // thread are on their way.  A thread owns whole pairs (both vectors of a
 // half-layout pair block), so x may be rotated in place.  Bound by memory: one
 // read and one write of every value (not in place: of the unrotated ones too).
 // VEC = 16 bytes of T where layout and alignment allow, else 1.
 template <typename T, int VEC, bool IL>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ __align__(16) float cs[128], sn[128];
-  const int tok = blockIdx.x;
-  const int pos = __ldg(p.pos + tok);
+__global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 && VEC > 1 ? 5 : 6) rope_kernel(const __grid_constant__ RopeParams p) {
+  extern __shared__ __align__(16) float2 turn[];   // cos, sin: [token][pair of a unit / 2][unit][2], so that lanes lie side by side
+  __shared__ int padding[kRopeTokens];
+  const int tok0 = blockIdx.x * p.tokens_per_cta, tokens = min(p.tokens_per_cta, p.tokens - tok0);
   const int half = p.rope.rot_dim >> 1, off = p.rope.offset, rot = p.rope.rot_dim;
   const int h0 = blockIdx.y * p.heads_per_cta, heads = min(p.heads_per_cta, p.heads - h0);
-  const T* x = reinterpret_cast<const T*>(p.x) + (long long)tok * p.x_token + (long long)h0 * p.x_head;
-  T* o = reinterpret_cast<T*>(p.out) + (long long)tok * p.o_token + (long long)h0 * p.o_head;
+  const T* x = reinterpret_cast<const T*>(p.x) + (long long)tok0 * p.x_token + (long long)h0 * p.x_head;
+  T* o = reinterpret_cast<T*>(p.out) + (long long)tok0 * p.o_token + (long long)h0 * p.o_head;
   // units of a head: rotated ones, then (not in place) the dimensions to copy
   constexpr int kPairs = IL ? (VEC > 1 ? VEC / 2 : 1) : VEC;   // pairs a rotated unit holds
   constexpr bool kOne = IL && VEC > 1;                         // a rotated unit is one vector, not two
-  constexpr int kAhead = kOne ? 4 : 2;                         // units that a thread has in flight
+  constexpr int kAhead = kOne ? 2 : 1;                         // units that a thread has in flight
   const int nrot = half / kPairs;
   const int ncopy = p.in_place ? 0 : (p.head_dim - rot) / VEC;
   const int units = nrot + ncopy;
-  const int step_h = kRopeThreads / units, step_u = kRopeThreads - step_h * units;
-  int h = threadIdx.x / units, u = threadIdx.x - h * units;
+  // a thread's units are kRopeThreads apart: (token, head, unit) steps on by (step_t, step_h, step_u) with carries
+  const int step = kRopeThreads / units, step_u = kRopeThreads - step * units, step_t = step / heads, step_h = step - step_t * heads;
+  const int row = threadIdx.x / units;
+  int t = row / heads, h = row - t * heads, u = threadIdx.x - row * units;
   using V = Vec<T, VEC>;
   bool first = true;
   // every thread meets the barrier below, also one without a unit
-  while (first || h < heads) {
+  while (first || t < tokens) {
     V a[kAhead], b[kAhead];
-    int at_h[kAhead], at_u[kAhead];
+    int at_t[kAhead], at_h[kAhead], at_u[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      at_h[k] = h, at_u[k] = u;
-      h += step_h, u += step_u;
+      at_t[k] = t, at_h[k] = h, at_u[k] = u;
+      u += step_u, h += step_h, t += step_t;
       if (u >= units) u -= units, ++h;
-      if (at_h[k] < heads) {
-        const T* xh = x + (long long)at_h[k] * p.x_head;
+      if (h >= heads) h -= heads, ++t;
+      if (at_t[k] < tokens) {
+        const T* xh = x + (long long)at_t[k] * p.x_token + (long long)at_h[k] * p.x_head;
         const int v = at_u[k];
         if (v >= nrot) {
           const int d = (v - nrot) * VEC;
@@ -105,24 +109,33 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     }
     if (first) {
       first = false;
-      for (int i = threadIdx.x; i < half; i += kRopeThreads) rope_cs(p.rope, i, pos, p.transpose, &cs[i], &sn[i]);
+      for (int i = threadIdx.x; i < tokens * half; i += kRopeThreads) {
+        const int tt = i / half, pair = i - tt * half, pos = __ldg(p.pos + tok0 + tt);
+        float2* to = turn + tt * half +
+                     (kPairs == 1 ? pair : ((pair % kPairs / 2) * nrot + pair / kPairs) * 2 + (pair & 1));
+        rope_cs(p.rope, pair, pos, p.transpose, &to->x, &to->y);
+        if (pair == 0) padding[tt] = pos < 0;
+      }
       __syncthreads();
-      if (pos < 0) return;   // padding
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (at_h[k] < heads) {
-        T* oh = o + (long long)at_h[k] * p.o_head;
+      if (at_t[k] < tokens && !padding[at_t[k]]) {
+        T* oh = o + (long long)at_t[k] * p.o_token + (long long)at_h[k] * p.o_head;
         const int v = at_u[k];
         if (v >= nrot) {
           const int d = (v - nrot) * VEC;
           *reinterpret_cast<V*>(oh + (d >= off ? d + rot : d)) = a[k];
           continue;
         }
-        const int d = off + v * (kOne ? VEC : IL ? 2 : kPairs), i0 = v * kPairs;
+        const int d = off + v * (kOne ? VEC : IL ? 2 : kPairs);
+        const float2* cs = turn + at_t[k] * half + (kPairs == 1 ? v : v * 2);
+        float4 two = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          const float c = cs[i0 + i], s = sn[i0 + i];
+          if (kPairs == 1) two.x = cs->x, two.y = cs->y;
+          else if (i % 2 == 0) two = *reinterpret_cast<const float4*>(cs + i * nrot);
+          const float c = i % 2 ? two.z : two.x, s = i % 2 ? two.w : two.y;
           T& t1 = a[k].v[kOne ? 2 * i : i];
           T& t2 = kOne ? a[k].v[(2 * i + 1) % VEC] : b[k].v[i % VEC];
           const float x1 = to_f(t1), x2 = to_f(t2);
