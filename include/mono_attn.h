@@ -51,7 +51,7 @@ typedef struct {
   double factor;     /* context stretch, >= 1 (unused by MONO_ROPE_NONE) */
   double beta_fast, beta_slow; /* YaRN: turns over orig_context at the ramp's ends, e.g. 32 and 1 */
   int orig_context;  /* YaRN: the context length before the stretch */
-  float attn_factor; /* multiplies the rotated values; 0 = 1, for YaRN 0.1 ln(factor) + 1 */
+  double attn_factor; /* multiplies the rotated values; 0 = 1, for YaRN 0.1 ln(factor) + 1 */
 } mono_rope_config;
 
 /* A prepared rotation: a plain value, filled by mono_rope_init and passed by
@@ -60,7 +60,7 @@ typedef struct {
  * revolution in binary64, so far positions keep full precision. */
 typedef struct {
   int rot_dim, offset, interleaved;
-  float factor;
+  double factor;
   double turns[128];
 } mono_rope;
 
@@ -176,7 +176,8 @@ int mono_attn_append(mono_attn_plan_t* plan, const mono_kv_cache* cache, const m
  * rotated; the new tokens' keys and values are in the cache already (append
  * comes first).  A row that sees nothing gives 0 (lse -infinity).  Rows j >=
  * n_new of a sequence, and padding sequences, leave out and lse as they were.
- * What lies in unseen tokens (NaN included) has no effect.  lse: fp32
+ * What lies in unseen tokens (NaN included) has no effect.  The address ranges
+ * of q and out may not meet, nor rows of out each other.  lse: fp32
  * [seqs][width][q_heads] contiguous, or NULL: the log of the sum of exp(logits).
  * Sums and softmax statistics are fp32; probabilities enter the products with
  * 11 bits (MONO_F32: 22). */
@@ -197,7 +198,7 @@ enum {
 };
 
 typedef struct {
-  int n_out;        /* rows of W, >= 1 */
+  int n_out;        /* rows of W, 1..2^30 */
   int n_in;         /* columns of W, a multiple of group */
   int format;       /* MONO_INT4 | MONO_MXFP4 */
   int group;        /* inputs a scale: a multiple of 32; 32 for MONO_MXFP4 */
@@ -222,12 +223,12 @@ int mono_proj_plan(const mono_proj_config* cfg, mono_proj_plan_t** out);
  *   scales [n_out][n_in / group] in scale_dtype, or e8m0 bytes (255 = NaN)
  *   zeros  uint8 [n_out][n_in / group], 0..15 (low nibble taken), or NULL when cfg.zeros is 0
  * Asynchronous on `stream`; the inputs may be freed after the stream reaches
- * this point. */
+ * this point, and steps on other streams must wait for it. */
 int mono_proj_pack(mono_proj_plan_t* plan, const void* codes, const void* scales, const void* zeros, void* stream);
 
 /* y[r][n] = sum_k x[r][k] W[n][k] for rows 0..8 (0 is a no-op), rows x_row
  * and y_row elements apart.  Products are exact and sums fp32; y is rounded
- * once.  x enters with 11 bits below each row's largest magnitude that one warp
+ * once (the sums of MONO_INT4 products to 1e-6 for MONO_BF16).  x enters with 11 bits below each row's largest magnitude that one warp
  * reads down to 2^-29 of it (bf16 is exact there), MONO_F32 with 22.  y may
  * not overlap x.  Uses no scratch: calls on one plan may overlap. */
 int mono_proj_step(mono_proj_plan_t* plan, int rows, const void* x, int64_t x_row, void* y, int64_t y_row,

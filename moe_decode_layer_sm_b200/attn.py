@@ -31,11 +31,11 @@ _vp, _i32, _i64, _f32, _f64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, cty
 class RopeConfig(ctypes.Structure):
     _fields_ = [(n, _i32) for n in ("rot_dim", "offset", "interleaved", "scaling")] + \
                [(n, _f64) for n in ("theta", "factor", "beta_fast", "beta_slow")] + \
-               [("orig_context", _i32), ("attn_factor", _f32)]
+               [("orig_context", _i32), ("attn_factor", _f64)]
 
 
 class RopeValue(ctypes.Structure):
-    _fields_ = [("rot_dim", _i32), ("offset", _i32), ("interleaved", _i32), ("factor", _f32), ("turns", _f64 * 128)]
+    _fields_ = [("rot_dim", _i32), ("offset", _i32), ("interleaved", _i32), ("factor", _f64), ("turns", _f64 * 128)]
 
 
 class AttnConfig(ctypes.Structure):

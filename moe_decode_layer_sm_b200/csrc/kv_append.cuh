@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kern
       double2 w = make_double2(1.0, 0.0);
       if (is_far) {
         w = turn_of(f * (double)a);
-        w.x *= (double)p.rope.factor, w.y *= (double)p.rope.factor;
+        w.x *= p.rope.factor, w.y *= p.rope.factor;
       }
       const int n = is_far ? n_far : n_near;
       double2* to = (is_far ? far : near) + turns.slot(pr);

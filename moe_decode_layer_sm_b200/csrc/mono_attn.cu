@@ -35,6 +35,7 @@ int guarded(F&& f) {
   try {
     return f();
   } catch (...) {
+    g_error.clear();
     return MONO_ERR_OOM;   // the strings and vectors here fail for want of memory only
   }
 }
@@ -121,7 +122,7 @@ extern "C" int mono_rope_init(const mono_rope_config* c, mono_rope* out) {
     if (c->scaling == MONO_ROPE_NTK && c->rot_dim == 2) why += "NTK scaling needs rot_dim above 2\n";
     if (c->scaling == MONO_ROPE_YARN && (c->orig_context < 1 || !(c->beta_slow > 0.0) || !(c->beta_fast > c->beta_slow)))
       why += "YaRN needs orig_context >= 1 and beta_fast > beta_slow > 0\n";
-    if (!std::isfinite(c->attn_factor)) why += "attn_factor must be finite\n";
+    if (!(std::fabs(c->attn_factor) <= 1e6)) why += "attn_factor must be between -1e6 and 1e6\n";
     if (!why.empty()) return fail(MONO_ERR_INVALID_ARG, "rope_init: " + why);
     const double two_pi = 6.283185307179586476925286766559;
     const int rot = c->rot_dim;
@@ -139,8 +140,7 @@ extern "C" int mono_rope_init(const mono_rope_config* c, mono_rope* out) {
     out->rot_dim = rot;
     out->offset = c->offset;
     out->interleaved = c->interleaved != 0;
-    out->factor = c->attn_factor != 0.f ? c->attn_factor
-                  : c->scaling == MONO_ROPE_YARN ? (float)(0.1 * std::log(c->factor) + 1.0) : 1.f;
+    out->factor = c->attn_factor != 0.0 ? c->attn_factor : c->scaling == MONO_ROPE_YARN ? 0.1 * std::log(c->factor) + 1.0 : 1.0;
     for (int i = 0; i < rot / 2; ++i) {
       double f = std::pow(theta, -2.0 * i / rot);
       if (c->scaling == MONO_ROPE_LINEAR) f /= c->factor;
@@ -650,7 +650,7 @@ extern "C" int mono_proj_plan(const mono_proj_config* c, mono_proj_plan_t** out)
       if (!ok) why += m + "\n";
     };
     const bool mx = c->format == MONO_MXFP4, f32 = c->dtype == MONO_F32;
-    need(c->n_out >= 1, "n_out must be at least 1");
+    need(c->n_out >= 1 && c->n_out <= 1 << 30, "n_out must be 1..2^30");
     need(mx || c->format == MONO_INT4, "format must be MONO_INT4 or MONO_MXFP4");
     need(c->group >= 32 && c->group % 32 == 0, "group must be a multiple of 32");
     need(!mx || c->group == 32, "group must be 32 for MONO_MXFP4");

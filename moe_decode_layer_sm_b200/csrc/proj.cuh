@@ -143,7 +143,10 @@ size_t proj_smem(int rows, int kb) {
 //          q 2^-24, one nibble further up q 2^-20, which the tensor cores
 //          take at full rate; the zero point comes off the group's sum,
 //          sum (q - z) x = sum q x - z sum x, with sum x found once
-// so an int4 code costs half a mask and no conversion.  A group's scale
+// so an int4 code costs half a mask and no conversion.  The matrix unit aligns
+// its sums by the operands' exponents, of which a subnormal has the wrong one:
+// that is worth 1e-6 of the result (2e-7 with normal operands), below bf16's
+// rounding, so only bf16 rows take it; fp32 rows make q a normal number.  A group's scale
 // multiplies the fp32 sum of its products.  The warps' sums are added in a
 // fixed order, then the cluster's, pushed to the CTA that writes the output:
 // no scratch, no atomics.
@@ -354,6 +357,16 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
             a[1] = w & 0x00F000F0u;
             a[2] = v & 0x000F000Fu;
             a[3] = v & 0x00F000F0u;
+            if (F32) {   // q itself: under the exponents of 1024 and, a nibble up, of 64
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                a[j] |= 0x64006400u;
+                const __half2 h = *reinterpret_cast<const __half2*>(&a[j]);
+                const __half2 q = j & 1 ? __hfma2(h, __floats2half2_rn(0.0625f, 0.0625f), __floats2half2_rn(-64.f, -64.f))
+                                        : __hadd2(h, __floats2half2_rn(-1024.f, -1024.f));
+                a[j] = *reinterpret_cast<const uint32_t*>(&q);
+              }
+            }
           }
 #pragma unroll
           for (int sp = 0; sp < kSplit; ++sp) {
@@ -386,7 +399,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float s = sc.get(i, e), up = e ? 1048576.f : 16777216.f;
+              const float s = sc.get(i, e), up = F32 ? 1.f : e ? 1048576.f : 16777216.f;
               const float z = ZP ? (float)(((i < 2 ? zp.x : zp.y) >> (16 * (i & 1) + 8 * e)) & 15u) : 8.f;
 #pragma unroll
               for (int r = 0; r < 2; ++r) {

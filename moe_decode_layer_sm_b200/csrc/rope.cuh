@@ -14,8 +14,9 @@ __device__ __forceinline__ void rope_cs(const mono_rope& r, int i, int pos, bool
   t -= rint(t);
   float sn, cs;
   sincospif(2.0f * (float)t, &sn, &cs);
-  *c = r.factor * cs;
-  *s = transpose ? -r.factor * sn : r.factor * sn;
+  const float f = (float)r.factor;
+  *c = f * cs;
+  *s = transpose ? -f * sn : f * sn;
 }
 
 template <typename T>

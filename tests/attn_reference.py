@@ -38,15 +38,15 @@ def rotate(x, pos, rope, transpose=False):
 def rotate_bound(x, rope, dtype):
     """|error| of each rotated value.  The angle enters sincospi as 2 t in fp32:
     |2 pi t| <= pi, so it is off by pi 2^-24; sin and cos by one more unit
-    (2^-23 for values up to 1), the factor, two products and a sum by a half
-    unit each: below 10 x 2^-24 (|x1| + |x2|) factor.  Then one rounding."""
+    (2^-23 for values up to 1), the factor (and its product), two products and a
+    sum by a half unit each: below 11 x 2^-24 (|x1| + |x2|) factor.  Then one rounding."""
     v = rope.value
     n = v.rot_dim // 2
     d = torch.arange(n, device=x.device)
     i1 = v.offset + (2 * d if v.interleaved else d)
     i2 = v.offset + (2 * d + 1 if v.interleaved else d + n)
     b = torch.zeros_like(x, dtype=torch.float64)
-    m = (x.double()[..., i1].abs() + x.double()[..., i2].abs()) * abs(v.factor) * 10 * 2.0 ** -24
+    m = (x.double()[..., i1].abs() + x.double()[..., i2].abs()) * abs(v.factor) * 11 * 2.0 ** -24
     b[..., i1] = m
     b[..., i2] = m
     return b * (1 + half_step(dtype))

@@ -80,7 +80,7 @@ GOOD_PROJ = dict(n_out=64, n_in=256, format=4, group=128, scale_dtype=1, zeros=0
 
 
 @pytest.mark.parametrize("kw,frag", [
-    (dict(n_out=0), "n_out"), (dict(n_in=0), "n_in"), (dict(n_in=192), "n_in"), (dict(format=2), "format"),
+    (dict(n_out=0), "n_out"), (dict(n_out=(1 << 30) + 1), "n_out"), (dict(n_in=0), "n_in"), (dict(n_in=192), "n_in"), (dict(format=2), "format"),
     (dict(group=48), "group"), (dict(group=0), "group"), (dict(format=3, group=128), "group must be 32"),
     (dict(format=3, group=32, zeros=1), "zeros"), (dict(scale_dtype=2), "scale_dtype"), (dict(dtype=3), "dtype"),
     (dict(n_in=128 * 4096), "too large"),
@@ -139,7 +139,7 @@ def test_prepared_rotation(attn, rot, scaling, factor):
     # a power, a division and a blend, each rounded to binary64
     np.testing.assert_allclose(got, _frequency(rot, 10000.0, scaling, factor), rtol=1e-13)
     want = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" else 1.0
-    assert abs(r.factor - want) <= 2.0 ** -24 * 2 and r.rot_dim == rot
+    assert abs(r.factor - want) <= 2.0 ** -52 * 2 and r.rot_dim == rot
     assert not any(r.turns[rot // 2:])
     assert attn.Rope(rot, attn_factor=0.5).value.factor == 0.5
 

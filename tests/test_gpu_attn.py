@@ -93,6 +93,26 @@ def test_rope_strides_padding_and_alignment(m):
     assert not torch.equal(fused[0, :256], before[0, :256])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,d,rot,offset,il", [(1, 128, 128, 0, False), (3, 64, 64, 0, True), (2, 128, 64, 64, False),
+                                                   (5, 80, 6, 10, True), (7, 256, 256, 0, False)])
+def test_rope_many_tokens(m, dtype, heads, d, rot, offset, il):
+    """Several tokens a CTA, padding among them, a last CTA that is not full."""
+    tokens = 10007
+    r = m.Rope(rot, offset=offset, interleaved=il)
+    x = normal((tokens, heads, d), DT[dtype], 9)
+    pos = torch.randint(-1000, 100000, (tokens,), dtype=torch.int32, device="cuda", generator=gen(10))
+    out = torch.full_like(x, 3.0)
+    m.rope(x, pos, r, out=out)
+    live = pos >= 0
+    want, bound = R.rotate(x, pos, r), R.rotate_bound(x, r, DT[dtype])
+    bound = torch.where(bound > 0, bound + R.half_step(DT[dtype]) * want.abs(), bound)
+    within(out[live], want[live], bound[live])
+    assert (out[~live] == 3.0).all()
+    m.rope(x, pos, r)
+    assert torch.equal(x[live], out[live])
+
+
 def test_rope_gradient(m):
     """transpose is the gradient: <rope(x), y> = <x, rope^T(y)>, and the
     difference of the inner product along a direction is the same."""
@@ -313,6 +333,23 @@ def test_attend_long(m, dtype, d, hq, hk):
 def test_attend_many_sequences(m):
     check_attend(m, "bf16", [1 + 13 * i for i in range(130)], [1] * 130, 1, 5, 1, 128, 16)
     check_attend(m, "f32", [7] * 200, [2] * 200, 2, 4, 4, 64, 16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,hq,hk,width,window", [(64, 4, 2, 1, 0), (64, 16, 2, 3, 40), (128, 10, 2, 1, 0), (128, 8, 2, 4, 0),
+                                                  (256, 4, 2, 2, 70), (256, 2, 2, 1, 0)])
+def test_attend_more_items_than_sms(m, dtype, d, hq, hk, width, window):
+    """Narrow CTAs: several items each, items over several CTAs, padding among them."""
+    lens = [1 + (37 * i) % 600 for i in range(90)]
+    new = [0 if i % 11 == 5 else 1 + i % width for i in range(90)]
+    check_attend(m, dtype, lens, new, width, hq, hk, d, 16, window=window)
+
+
+def test_attend_short_tables(m):
+    """No sequence longer than a narrow CTA's round."""
+    check_attend(m, "bf16", [1, 16, 9], [1, 1, 1], 1, 40, 8, 128, 16)
+    check_attend(m, "f32", [1, 3, 2], [1, 3, 3], 3, 8, 8, 64, 16)
+    check_attend(m, "bf16", [1], [1], 1, 1, 1, 256, 16)
 
 
 def test_attend_large_logits_and_scales(m):
@@ -591,6 +628,49 @@ def test_other_streams_and_two_plans_at_once(m):
                     p.attend(c, q, lens, tab, o[j])
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for os, w in zip(outs, want) for o in os)
+
+
+def test_projection_and_append_share_a_plan_across_streams(m):
+    """Neither has scratch: calls on one plan that overlap in time."""
+    plan = m.Projection(640, 512, group=64, zeros=True)
+    w = make_weights(640, 512, "int4", 64, "bf16", True, 150)
+    plan.pack(*w)
+    xs = [normal((4, 512), torch.bfloat16, 151 + i) for i in range(2)]
+    want = [plan.step(x, torch.empty(4, 640, dtype=torch.bfloat16, device="cuda")) for x in xs]
+    attn = m.AttnPlan(2, 2, 64, 16, 8, 1, 4)
+    caches = [make_cache(m, 8, 2, 16, 64, 160) for _ in range(4)]
+    kv = [normal((1, 1, 2, 64), torch.bfloat16, 170 + i) for i in range(2)]
+    lens, table, rope = i32([33]), i32([[0, 1, 2, 3]]), m.Rope(64)
+    for c, k in zip(caches[:2], kv):
+        attn.append(c, k, k, lens, table, rope=rope)
+    ys = [[torch.empty_like(want[0]) for _ in range(10)] for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for j in range(10):
+        for i, st in enumerate(streams):
+            plan.step(xs[i], ys[i][j], stream=st)
+            if j == 5:
+                attn.append(caches[2 + i], kv[i], kv[i], lens, table, rope=rope, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in ys[i])
+    for i in range(2):
+        assert torch.equal(caches[i].k.view(torch.uint8), caches[2 + i].k.view(torch.uint8))
+        assert torch.equal(caches[i].v_scale, caches[2 + i].v_scale)
+
+
+def test_packing_again_replaces_the_weights(m):
+    plan = m.Projection(100, 64, fmt="mxfp4", group=32)
+    x, y = normal((2, 64), torch.bfloat16, 180), torch.empty(2, 100, dtype=torch.bfloat16, device="cuda")
+    for seed, special in ((181, True), (182, False)):   # scales of 0 and 255 first, then none
+        codes, scales, _ = make_weights(100, 64, "mxfp4", 32, None, False, seed)
+        if special:
+            scales[3, 0], scales[4, 1] = 255, 0
+        plan.pack(codes, scales)
+        plan.step(x, y)
+        want, bound = R.project(x, R.weights(codes, scales, None, "mxfp4", 32))
+        keep = torch.arange(100, device="cuda") != (3 if special else -1)
+        within(y[:, keep], want[:, keep], bound[:, keep])
+        assert torch.isnan(y[:, 3]).all() == special
 
 
 def test_captured_decode_serves_growing_lengths(m):
