@@ -3,13 +3,14 @@ rotary positions, the append to a paged 8-bit cache, attention over it and the
 4-bit projections.
 
 Argument checks and marshalling only; every operator runs in the library's
-CUDA kernels.  Tensors are CUDA tensors of the plan's device, the last
+CUDA kernels.  The calls of a decode step (rope, append, attend, step) check and
+marshal in a compiled module (csrc/call.cpp); where it takes a call for wrong,
+the reasons are found here.  Tensors are CUDA tensors of the plan's device, the last
 dimension contiguous, other strides free where the text says so.  Calls run on
 the current stream of that device unless `stream` is given.
 """
 
 import ctypes
-import struct
 
 import torch
 
@@ -47,11 +48,6 @@ class CacheStruct(ctypes.Structure):
     _fields_ = [(n, _vp) for n in ("k", "v", "k_scale", "v_scale")]
 
 
-# mono_rows and mono_seqs of a call, as the bytes that the library reads
-_rows = struct.Struct("@Pqqq").pack
-_seqs = struct.Struct("@iiPPP").pack
-
-
 class AttnInfo(ctypes.Structure):
     _fields_ = [("grid", _i32), ("scratch_bytes", _i64)]
 
@@ -69,10 +65,11 @@ class ProjInfo(ctypes.Structure):
 
 
 _ready = None
+_call = None   # the compiled module
 
 
 def _lib():
-    global _ready
+    global _ready, _call
     if _ready is None:
         L = lib()
         P = ctypes.POINTER
@@ -94,7 +91,8 @@ def _lib():
             getattr(L, f).restype = None
         L.mono_attn_last_error.argtypes = []
         L.mono_attn_last_error.restype = ctypes.c_char_p
-        _ready = L
+        from . import _call as compiled
+        _call, _ready = compiled, L
     return _ready
 
 
@@ -103,13 +101,8 @@ def _check(rc):
         raise MonoError(rc, _lib().mono_attn_last_error().decode())
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the current stream's handle, without an object for it
-
-
 def _stream_of(device, stream):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch.cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device)
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream.cuda_stream
 
 
 def _refuse(who, why):
@@ -143,27 +136,10 @@ def rope(x, positions, rope, out=None, transpose=False, stream=None):
     row, left as it was).  out None rotates in place.  transpose applies the
     transposed map (the gradient's).  Returns out."""
     out = x if out is None else out
-    dev = x.get_device()
-    try:
-        tokens, heads, head_dim = x.shape
-        xt, xh, xd = x.stride()
-        ot, oh, od = out.stride()
-        ok = (dev >= 0 and positions.get_device() == dev and out.get_device() == dev and out.dtype is x.dtype
-              and positions.dtype is torch.int32 and positions.shape == (tokens,) and positions.is_contiguous()
-              and (out is x or out.shape == x.shape) and ((xd == 1 and od == 1) or not tokens or not heads)
-              and x.dtype in _CODE)
-    except ValueError:   # other numbers of dimensions
-        ok = False
-    if not ok:
-        _refuse_rope(x, positions, out)
-    call = (rope._at, tokens, heads, head_dim, _CODE[x.dtype], x.data_ptr(), xt, xh, positions.data_ptr(),
-            out.data_ptr(), ot, oh, 1 if transpose else 0, _stream_of(dev, stream))
-    if torch._C._cuda_getDevice() == dev:
-        rc = _lib().mono_rope_apply(*call)
-    else:
-        with torch.cuda.device(dev):
-            rc = _lib().mono_rope_apply(*call)
+    rc = _call.rope(rope._at, x, positions, out, transpose, None if stream is None else stream.cuda_stream)
     if rc:
+        if rc == _call.NOT_TAKEN:
+            _refuse_rope(x, positions, out)
         _check(rc)
     return out
 
@@ -233,16 +209,7 @@ class AttnPlan:
         self.dtype, self.device = _NAME[dtype], device
         self.shape = (num_pages, kv_heads, page_size, head_dim)
         self.q_heads, self.kv_heads, self.head_dim, self.max_pages = q_heads, kv_heads, head_dim, max_pages
-        self._append, self._attend = self._lib.mono_attn_append, self._lib.mono_attn_attend
-
-    def _seqs_ok(self, cache, n, lens, table, n_new):
-        """Whether the cache and the entries of a call's n sequences are what they must be."""
-        dev, i32 = self.device, torch.int32
-        return (cache.shape == self.shape and cache.device == dev and lens.dtype is i32 and lens.shape == (n,)
-                and lens.get_device() == dev and lens.is_contiguous() and table.dtype is i32
-                and table.shape == (n, self.max_pages) and table.get_device() == dev and table.is_contiguous()
-                and (n_new is None or (n_new.dtype is i32 and n_new.shape == (n,) and n_new.get_device() == dev
-                                       and n_new.is_contiguous())))
+        self._at, self._code = h.value, self.cfg.dtype
 
     def _refuse(self, who, names, cache, x, heads, y, lens, table, n_new):
         why, d = [], self.device
@@ -273,45 +240,30 @@ class AttnPlan:
         into the pages of `table` [seqs][max_pages]; lens [seqs] counts the new
         tokens, n_new [seqs] says how many of the rows are new (None: all).
         rope: the keys are rotated to their positions on the way."""
-        shape, dtype, dev = k.shape, self.dtype, self.device
-        if len(shape) != 4 or v.shape != shape:
+        if cache.shape != self.shape or cache.device != self.device:
             self._refuse("append", ("k", "v"), cache, k, self.kv_heads, v, lens, table, n_new)
-        n, width, heads, head_dim = shape
-        ks, kt, kh, kd = k.stride()
-        vs, vt, vh, vd = v.stride()
-        if not (heads == self.kv_heads and head_dim == self.head_dim and kd == 1 and vd == 1 and k.dtype is dtype
-                and v.dtype is dtype and k.get_device() == dev and v.get_device() == dev
-                and self._seqs_ok(cache, n, lens, table, n_new)):
-            self._refuse("append", ("k", "v"), cache, k, self.kv_heads, v, lens, table, n_new)
-        rc = self._append(self.handle, cache._at,
-                          _seqs(n, width, lens.data_ptr(), 0 if n_new is None else n_new.data_ptr(), table.data_ptr()),
-                          _rows(k.data_ptr(), ks, kt, kh), _rows(v.data_ptr(), vs, vt, vh),
-                          None if rope is None else rope._at, _stream_of(dev, stream))
+        rc = _call.append(self._at, cache._at, self.kv_heads, self.head_dim, self._code, self.device, self.max_pages,
+                          k, v, lens, table, n_new, None if rope is None else rope._at,
+                          None if stream is None else stream.cuda_stream)
         if rc:
+            if rc == _call.NOT_TAKEN:
+                self._refuse("append", ("k", "v"), cache, k, self.kv_heads, v, lens, table, n_new)
             _check(rc)
 
     def attend(self, cache, q, lens, table, out, lse=None, n_new=None, stream=None):
         """mono_attn_attend: out [seqs][width][q_heads][head_dim] of q (rotated; the
         same shape, strides free) over the cached tokens that each row sees.  lse:
         fp32 [seqs][width][q_heads], the log of the sum of exponentials.  Returns out."""
-        shape, dtype, dev = q.shape, self.dtype, self.device
-        if len(shape) != 4 or out.shape != shape:
+        if cache.shape != self.shape or cache.device != self.device:
             self._refuse("attend", ("q", "out"), cache, q, self.q_heads, out, lens, table, n_new)
-        n, width, heads, head_dim = shape
-        qs, qt, qh, qd = q.stride()
-        os, ot, oh, od = out.stride()
-        if not (heads == self.q_heads and head_dim == self.head_dim and qd == 1 and od == 1 and q.dtype is dtype
-                and out.dtype is dtype and q.get_device() == dev and out.get_device() == dev
-                and self._seqs_ok(cache, n, lens, table, n_new)):
-            self._refuse("attend", ("q", "out"), cache, q, self.q_heads, out, lens, table, n_new)
-        if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:3] or not lse.is_contiguous()
-                                or lse.get_device() != dev):
-            raise ValueError("attend: lse must be contiguous fp32 [seqs][width][q_heads] on the plan's device")
-        rc = self._attend(self.handle, cache._at,
-                          _seqs(n, width, lens.data_ptr(), 0 if n_new is None else n_new.data_ptr(), table.data_ptr()),
-                          _rows(q.data_ptr(), qs, qt, qh), _rows(out.data_ptr(), os, ot, oh),
-                          None if lse is None else lse.data_ptr(), _stream_of(dev, stream))
+        rc = _call.attend(self._at, cache._at, self.q_heads, self.head_dim, self._code, self.device, self.max_pages,
+                          q, out, lens, table, n_new, lse, None if stream is None else stream.cuda_stream)
         if rc:
+            if rc == _call.NOT_TAKEN:
+                if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3]
+                                        or not lse.is_contiguous() or lse.get_device() != self.device):
+                    raise ValueError("attend: lse must be contiguous fp32 [seqs][width][q_heads] on the plan's device")
+                self._refuse("attend", ("q", "out"), cache, q, self.q_heads, out, lens, table, n_new)
             _check(rc)
         return out
 
@@ -332,7 +284,7 @@ class AttnPlan:
     def close(self):
         if getattr(self, "handle", None):
             self._lib.mono_attn_destroy(self.handle)
-            self.handle = None
+            self.handle, self._at = None, 0
 
     def __del__(self):
         try:
@@ -363,7 +315,7 @@ class Projection:
         self.dtype, self.device = _NAME[dtype], device
         self.scale_dtype = torch.uint8 if mx else _NAME[scale_dtype]
         self.n_out, self.n_in, self.group, self.zeros = n_out, n_in, group, bool(zeros)
-        self._step = self._lib.mono_proj_step
+        self._at = h.value
 
     def pack(self, codes, scales, zeros=None, stream=None):
         """codes uint8 [n_out][n_in / 2] (the even input in the low nibble), scales
@@ -386,16 +338,11 @@ class Projection:
 
     def step(self, x, y, stream=None):
         """y [rows][n_out] = x [rows][n_in] W^T, up to 8 rows, row strides free.  Returns y."""
-        shape, dtype, dev = x.shape, self.dtype, self.device
-        if len(shape) != 2 or shape[1] != self.n_in or y.shape != (shape[0], self.n_out):
-            self._refuse_step(x, y)
-        xr, xd = x.stride()
-        yr, yd = y.stride()
-        if not (xd == 1 and (yd == 1 or self.n_out == 1) and x.dtype is dtype and y.dtype is dtype
-                and x.get_device() == dev and y.get_device() == dev):
-            self._refuse_step(x, y)
-        rc = self._step(self.handle, shape[0], x.data_ptr(), xr, y.data_ptr(), yr, _stream_of(dev, stream))
+        rc = _call.step(self._at, self.n_out, self.n_in, self.cfg.dtype, self.device, x, y,
+                        None if stream is None else stream.cuda_stream)
         if rc:
+            if rc == _call.NOT_TAKEN:
+                self._refuse_step(x, y)
             _check(rc)
         return y
 
@@ -419,7 +366,7 @@ class Projection:
     def close(self):
         if getattr(self, "handle", None):
             self._lib.mono_proj_destroy(self.handle)
-            self.handle = None
+            self.handle, self._at = None, 0
 
     def __del__(self):
         try:

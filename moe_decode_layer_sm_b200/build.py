@@ -4,11 +4,16 @@ package so that the library travels with the source tree.
 The library is rebuilt unless a stamp file beside it records the SHA-256 of
 every source it is built from and of the nvcc commands: a binary that merely
 has a later modification time than its sources is not trusted.  Each
-translation unit keeps an object with a stamp of its own."""
+translation unit keeps an object with a stamp of its own.
+
+_call.so, the compiled part of the attention half's binding, is built beside it
+with g++ against the installed torch and has its own stamp."""
 
 import hashlib
 import os
 import subprocess
+import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -73,11 +78,51 @@ def up_to_date():
         return f.read().strip() == source_hash()
 
 
+CALL = os.path.join(PKG, "_call.so")
+CALL_SOURCES = ["call.cpp", "mono_attn.h", "mono_ffn.h"]
+
+
+def call_command():
+    import torch
+    t = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE, *[f"-isystem{p}" for p in inc],
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-o", CALL, _path("call.cpp"),
+            "-L", PKG, "-l:libmonoffn.so", "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda",
+            "-lc10", "-Wl,-rpath,$ORIGIN"]
+
+
+def call_hash():
+    import torch
+    h = hashlib.sha256()
+    for d in CALL_SOURCES:
+        with open(_path(d), "rb") as f:
+            h.update(f.read())
+    h.update(" ".join([torch.__version__, sys.version, *call_command()]).encode())
+    return h.hexdigest()
+
+
+def build_call(force=False):
+    stamp = CALL + ".sha256"
+    if not force and os.path.exists(CALL) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == call_hash():
+                return CALL
+    if os.path.exists(stamp):
+        os.unlink(stamp)
+    _run(call_command())
+    with open(stamp, "w") as f:
+        f.write(call_hash() + "\n")
+    return CALL
+
+
 def _run(cmd):
     res = subprocess.run(cmd, capture_output=True, text=True)
     log = " ".join(cmd) + "\n" + res.stdout + res.stderr
     if res.returncode != 0:
-        raise RuntimeError("nvcc failed:\n" + log[-4000:])
+        raise RuntimeError(f"{cmd[0]} failed:\n" + log[-4000:])
     return log
 
 
@@ -98,6 +143,7 @@ def _compile(unit, force):
 
 def build(force=False, verbose=False):
     if not force and up_to_date():
+        build_call()
         return SO
     if os.path.exists(STAMP):
         os.unlink(STAMP)
@@ -108,6 +154,7 @@ def build(force=False, verbose=False):
         f.write(log)
     with open(STAMP, "w") as f:
         f.write(source_hash() + "\n")
+    build_call(force)
     if verbose:
         print(log)
     return SO

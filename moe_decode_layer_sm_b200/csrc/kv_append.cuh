@@ -183,6 +183,10 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 // the others by turning; a thread holds both halves of its pairs, so a value
 // costs one conversion each way and four binary64 operations.
 //
+// Measured: 10486 tokens of 4 prompts, 8 heads of 128, bf16, rotated 43 us, not
+// rotated 32 (64 MB: 10 us of memory); bound by instructions, of which a head's
+// and a CTA's own are more than the values'.  One token of 8 sequences 3.6 us.
+//
 // U: units of 16 values that a thread holds of a page's head.  EACH: rotations
 // whose offset or halves no vector of eight respects.
 template <typename T, int U, bool EACH>

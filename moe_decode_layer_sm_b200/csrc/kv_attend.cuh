@@ -199,6 +199,12 @@ struct QRows {
 // the device, so one captured launch serves any lengths.  An item that spans CTAs leaves partial (O, m, l)
 // in the scratch, and the CTA that arrives last joins them in a fixed order:
 // results do not depend on the order of arrival.
+//
+// Measured, heads 40 / 8 of 128, bf16: one sequence of 131071 tokens 62 us
+// (its rounds run at 7.0 TB/s; 3 us lie before the first copy, 10 behind the
+// last), 8 sequences to 8192 tokens 28 us, one token 7.6 us.  Registers are
+// kept free of spills: with the rings in shared memory little L1 is left, and
+// 50 spilled words a tile took a third of the time.
 template <int D, int NT, bool F32, int W>
 __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) / 4)
     attend_kernel(const __grid_constant__ AttendParams p) {

@@ -135,7 +135,8 @@ size_t proj_smem(int rows, int kb) {
 // warp streams its weights through a ring of its own in shared memory by
 // asynchronous copies, kProjDepth blocks ahead and across output blocks: in
 // registers the same depth stalled, since a warp's few scoreboards tie the
-// loads of different blocks together (224 us for 131072 x 5120 MXFP4, 8 rows).
+// loads of different blocks together (131072 x 5120 MXFP4, 8 rows: 142 us, and
+// 97 through the ring).
 // x is converted once a CTA, each row of a warp's part scaled by a power of
 // two to fp16's range (fp32 as two terms).  Codes become exact fp16 operands:
 //   e2m1   by the pair converter
@@ -150,6 +151,11 @@ size_t proj_smem(int rows, int kb) {
 // multiplies the fp32 sum of its products.  The warps' sums are added in a
 // fixed order, then the cluster's, pushed to the CTA that writes the output:
 // no scratch, no atomics.
+//
+// Measured: 131072 x 5120 MXFP4, 8 rows, 77 us (4.6 TB/s; the pair converter
+// and the scales keep the integer pipe busy, 158 instructions for 2048 codes);
+// 7168 x 5120 int4, 1 row, 9.8 us (2.4 until x is ready, 3.7 of weights at
+// 5.1 TB/s on the 112 SMs that have an output block).
 template <bool F32, int SC, bool ZP>
 __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_constant__ ProjParams p) {
   namespace cg = cooperative_groups;

@@ -62,6 +62,9 @@ constexpr int kRopeTokens = 16;   // of a CTA at most
 // thread are on their way.  A thread owns whole pairs (both vectors of a
 // half-layout pair block), so x may be rotated in place.  Bound by memory: one
 // read and one write of every value (not in place: of the unrotated ones too).
+// Measured, 8191 x 40 heads of 128: fp32 halves 51 us (6.6 TB/s), fp32
+// interleaved half of the head 61, bf16 halves 32 and interleaved 42 (5.2 and
+// 4.0 TB/s: there the instructions weigh as much as the bytes).
 // VEC = 16 bytes of T where layout and alignment allow, else 1.
 template <typename T, int VEC, bool IL>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 && VEC > 1 ? 5 : 6) rope_kernel(const __grid_constant__ RopeParams p) {
