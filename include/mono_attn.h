@@ -75,7 +75,7 @@ int mono_rope_init(const mono_rope_config* cfg, mono_rope* out);
  * pos[t] < 0 marks a padding row: out is left as it was.  Computed in fp32,
  * rounded once.  dtype MONO_F32 | MONO_BF16 for both.  out may be x itself
  * (same strides); any other overlap of their address ranges is refused, and so
- * is an out whose rows overlap.  heads <= 65536, head_dim <= 1024. */
+ * is an out whose rows overlap.  heads <= 65535, head_dim <= 1024. */
 int mono_rope_apply(const mono_rope* rope, int tokens, int heads, int head_dim, int dtype, const void* x,
                     int64_t x_token, int64_t x_head, const int* pos, void* out, int64_t out_token, int64_t out_head,
                     int transpose, void* stream);

@@ -183,7 +183,7 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 // the others by turning; a thread holds both halves of its pairs, so a value
 // costs one conversion each way and four binary64 operations.
 //
-// Measured: 10486 tokens of 4 prompts, 8 heads of 128, bf16, rotated 43 us, not
+// Measured: 10486 tokens of 4 prompts, 8 heads of 128, bf16, rotated 42 us, not
 // rotated 32 (64 MB: 10 us of memory); bound by instructions, of which a head's
 // and a CTA's own are more than the values'.  One token of 8 sequences 3.6 us.
 //
@@ -410,21 +410,12 @@ __global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kern
             const bool turned = !PLAIN && (EACH || (mode == kHalves ? pair[u] >= 0 : d >= off && d < off + rot));
             unsigned int near = 0u;
             float y[8];
-            bool small = false;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              y[i] = val[u][8 * v + i] * rs;
-              small |= fabsf(y[i]) < 0.015625f;
-            }
+            for (int i = 0; i < 8; ++i) y[i] = val[u][8 * v + i] * rs;
             if (!turned && !exact) {   // the values as they came: bf16's meet borders often
-              if (small) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  y[i] = fp8_place(y[i], val[u][8 * v + i], sc, fabsf(y[i]) < 0.015625f ? 0.015625f : 0.f);
-              } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = fp8_place(y[i], val[u][8 * v + i], sc, 0.f);
-              }
+              for (int i = 0; i < 8; ++i)
+                y[i] = fp8_place(y[i], val[u][8 * v + i], sc, fabsf(y[i]) < 0.015625f ? 0.015625f : 0.f);
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i)

@@ -180,7 +180,7 @@ extern "C" int mono_rope_apply(const mono_rope* rope, int tokens, int heads, int
     std::string why;
     if (!rope) return fail(MONO_ERR_INVALID_ARG, "rope_apply: NULL rope");
     if (tokens < 0) why += "tokens must not be negative\n";
-    if (heads < 0 || heads > 65536) why += "heads must be 0..65536\n";
+    if (heads < 0 || heads > 65535) why += "heads must be 0..65535\n";
     if (head_dim < 2 || head_dim > 1024) why += "head_dim must be 2..1024\n";
     if (dtype != MONO_F32 && dtype != MONO_BF16) why += "dtype must be MONO_F32 or MONO_BF16\n";
     why += rope_reasons(rope, head_dim);
@@ -215,6 +215,11 @@ extern "C" int mono_rope_apply(const mono_rope* rope, int tokens, int heads, int
     int parts = 1;
     if (tokens < 2 * kSms) parts = std::min(heads, (2 * kSms + tokens - 1) / tokens);
     p.heads_per_cta = (heads + parts - 1) / parts;
+    // places within a CTA are 32-bit; strides that pass that leave it one row
+    const auto reach = [&](int64_t token, int64_t head) {
+      return (double)p.tokens_per_cta * std::fabs((double)token) + (double)p.heads_per_cta * std::fabs((double)head) + head_dim;
+    };
+    if (std::max(reach(x_token, x_head), reach(out_token, out_head)) >= 1073741824.0) p.tokens_per_cta = p.heads_per_cta = 1;
     const dim3 grid((tokens + p.tokens_per_cta - 1) / p.tokens_per_cta, (heads + p.heads_per_cta - 1) / p.heads_per_cta);
     cudaStream_t st = (cudaStream_t)stream;
     if (dtype == MONO_BF16) {

@@ -62,9 +62,9 @@ constexpr int kRopeTokens = 16;   // of a CTA at most
 // thread are on their way.  A thread owns whole pairs (both vectors of a
 // half-layout pair block), so x may be rotated in place.  Bound by memory: one
 // read and one write of every value (not in place: of the unrotated ones too).
-// Measured, 8191 x 40 heads of 128: fp32 halves 51 us (6.6 TB/s), fp32
-// interleaved half of the head 61, bf16 halves 32 and interleaved 42 (5.2 and
-// 4.0 TB/s: there the instructions weigh as much as the bytes).
+// Measured, 8191 x 40 heads of 128: fp32 53 us (6.3 TB/s; 61 with 64-bit places
+// found for each unit), bf16 halves 32 and interleaved 34 (5 TB/s: there the
+// instructions weigh as much as the bytes).
 // VEC = 16 bytes of T where layout and alignment allow, else 1.
 template <typename T, int VEC, bool IL>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 && VEC > 1 ? 5 : 6) rope_kernel(const __grid_constant__ RopeParams p) {
@@ -82,34 +82,36 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 && VEC > 1 ? 5 : 
   const int nrot = half / kPairs;
   const int ncopy = p.in_place ? 0 : (p.head_dim - rot) / VEC;
   const int units = nrot + ncopy;
-  // a thread's units are kRopeThreads apart: (token, head, unit) steps on by (step_t, step_h, step_u) with carries
+  // a thread's units are kRopeThreads apart: (token, head, unit) and the rows'
+  // places, which fit 32 bits within a CTA, step on by sums with carries
   const int step = kRopeThreads / units, step_u = kRopeThreads - step * units, step_t = step / heads, step_h = step - step_t * heads;
+  const int xt = (int)p.x_token, xh = (int)p.x_head, ot = (int)p.o_token, oh = (int)p.o_head;
+  const int step_x = step_t * xt + step_h * xh, step_o = step_t * ot + step_h * oh;
+  const int wrap_x = xt - heads * xh, wrap_o = ot - heads * oh;
   const int row = threadIdx.x / units;
   int t = row / heads, h = row - t * heads, u = threadIdx.x - row * units;
+  int xo = t * xt + h * xh, oo = t * ot + h * oh;
   using V = Vec<T, VEC>;
   bool first = true;
   // every thread meets the barrier below, also one without a unit
   while (first || t < tokens) {
     V a[kAhead], b[kAhead];
-    int at_t[kAhead], at_h[kAhead], at_u[kAhead];
+    int at_t[kAhead], at_u[kAhead], to[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      at_t[k] = t, at_h[k] = h, at_u[k] = u;
-      u += step_u, h += step_h, t += step_t;
-      if (u >= units) u -= units, ++h;
-      if (h >= heads) h -= heads, ++t;
-      if (at_t[k] < tokens) {
-        const T* xh = x + (long long)at_t[k] * p.x_token + (long long)at_h[k] * p.x_head;
-        const int v = at_u[k];
-        if (v >= nrot) {
-          const int d = (v - nrot) * VEC;
-          a[k] = *reinterpret_cast<const V*>(xh + (d >= off ? d + rot : d));
-        } else {
-          const int d = off + v * (kOne ? VEC : IL ? 2 : kPairs);
-          a[k] = *reinterpret_cast<const V*>(xh + d);
-          if (!kOne) b[k] = *reinterpret_cast<const V*>(xh + (IL ? d + 1 : d + half));
-        }
+      at_t[k] = t, at_u[k] = u;
+      // the first dimension of the unit
+      const int c = (u - nrot) * VEC;
+      const int d = u < nrot ? off + u * (kOne ? VEC : IL ? 2 : kPairs) : c >= off ? c + rot : c;
+      to[k] = oo + d;
+      if (t < tokens) {
+        const T* from = x + (xo + d);
+        a[k] = *reinterpret_cast<const V*>(from);
+        if (!kOne && u < nrot) b[k] = *reinterpret_cast<const V*>(from + (IL ? 1 : half));
       }
+      u += step_u, h += step_h, t += step_t, xo += step_x, oo += step_o;
+      if (u >= units) u -= units, ++h, xo += xh, oo += oh;
+      if (h >= heads) h -= heads, ++t, xo += wrap_x, oo += wrap_o;
     }
     if (first) {
       first = false;
@@ -125,14 +127,11 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 && VEC > 1 ? 5 : 
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
       if (at_t[k] < tokens && !padding[at_t[k]]) {
-        T* oh = o + (long long)at_t[k] * p.o_token + (long long)at_h[k] * p.o_head;
         const int v = at_u[k];
         if (v >= nrot) {
-          const int d = (v - nrot) * VEC;
-          *reinterpret_cast<V*>(oh + (d >= off ? d + rot : d)) = a[k];
+          *reinterpret_cast<V*>(o + to[k]) = a[k];
           continue;
         }
-        const int d = off + v * (kOne ? VEC : IL ? 2 : kPairs);
         const float2* cs = turn + at_t[k] * half + (kPairs == 1 ? v : v * 2);
         float4 two = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -146,8 +145,8 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(T) == 2 && VEC > 1 ? 5 : 
           t1 = from_f<T>(c * x1 - s * x2);
           t2 = from_f<T>(s * x1 + c * x2);
         }
-        *reinterpret_cast<V*>(oh + d) = a[k];
-        if (!kOne) *reinterpret_cast<V*>(oh + (IL ? d + 1 : d + half)) = b[k];
+        *reinterpret_cast<V*>(o + to[k]) = a[k];
+        if (!kOne) *reinterpret_cast<V*>(o + to[k] + (IL ? 1 : half)) = b[k];
       }
   }
 }

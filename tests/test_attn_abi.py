@@ -171,7 +171,7 @@ def test_rope_apply_refuses(attn):
         rc = L.mono_rope_apply(r._at if at is None else at, tokens, heads, head_dim, dtype, x, *xs, pos, out, *os, 0, None)
         return rc, L.mono_attn_last_error().decode()
 
-    for kw, frag in [(dict(tokens=-1), "tokens"), (dict(heads=65537), "heads"), (dict(head_dim=1025), "head_dim"),
+    for kw, frag in [(dict(tokens=-1), "tokens"), (dict(heads=65536), "heads"), (dict(head_dim=1025), "head_dim"),
                      (dict(head_dim=126), "passes the head's end"), (dict(dtype=2), "dtype"), (dict(x=None), "NULL"),
                      (dict(pos=None), "NULL"), (dict(out=4096, os=(512, 128)), "in place"), (dict(out=4096 + 512), "overlap"),
                      (dict(os=(0, 128)), "rows of out"), (dict(os=(256, 64)), "rows of out"),

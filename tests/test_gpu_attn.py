@@ -113,6 +113,20 @@ def test_rope_many_tokens(m, dtype, heads, d, rot, offset, il):
     assert torch.equal(x[live], out[live])
 
 
+def test_rope_far_strides(m):
+    """Rows further apart than 32 bits count."""
+    store = torch.zeros(2 ** 31 + 4096, dtype=torch.bfloat16, device="cuda")
+    x = store.as_strided((2, 3, 64), (2 ** 31, 64, 1))
+    x.copy_(normal((2, 3, 64), torch.bfloat16, 14))
+    r, pos = m.Rope(64), i32([7, 900])
+    want, bound = R.rotate(x, pos, r), R.rotate_bound(x, r, x.dtype)
+    out = torch.empty(2, 3, 64, dtype=torch.bfloat16, device="cuda")
+    m.rope(x, pos, r, out=out)
+    within(out, want, bound + R.half_step(x.dtype) * want.abs())
+    m.rope(x, pos, r)
+    assert torch.equal(x, out)
+
+
 def test_rope_gradient(m):
     """transpose is the gradient: <rope(x), y> = <x, rope^T(y)>, and the
     difference of the inner product along a direction is the same."""
