@@ -165,7 +165,8 @@ int mono_attn_plan(const mono_attn_config* cfg, mono_attn_plan_t** out);
  *        (the rotated key x in binary64: codes are rounded once)
  *   older codes become e4m3(code s / s') where s' > s
  * Slots behind the new tokens keep their bytes, and the scale of an untouched
- * page stays.  A page that a call writes belongs to one sequence of the call.
+ * page stays.  A page that a call writes stands once in the call's tables (a
+ * page that is only read, as a shared prefix by attend, may stand in many).
  * width is not limited by max_new.  Tokens at negative positions (lens <
  * n_new) are not written. */
 int mono_attn_append(mono_attn_plan_t* plan, const mono_kv_cache* cache, const mono_seqs* seqs, const mono_rows* k,

@@ -12,6 +12,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// D = A B, from zero
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // 8 x 8 transpose of 16-bit values across a warp
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
@@ -654,9 +661,17 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
             e4m3x4_to_h2(x0, a[0], a[1]);
             e4m3x4_to_h2(x1, a[2], a[3]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+              if (F32) {   // the matrix unit cuts what it adds up; fp32 rows round instead
+                float o[4];
+                mma_f16_first(o, a, pf[b][n][0][0], pf[b][n][0][1]);
+                mma_f16(o, a, pf[b][n][kSplit - 1][0], pf[b][n][kSplit - 1][1]);
 #pragma unroll
-              for (int sp = 0; sp < kSplit; ++sp) mma_f16(O[w][n], a, pf[b][n][sp][0], pf[b][n][sp][1]);
+                for (int j = 0; j < 4; ++j) O[w][n][j] += o[j];
+              } else {
+                mma_f16(O[w][n], a, pf[b][n][0][0], pf[b][n][0][1]);
+              }
+            }
           }
         }
       }

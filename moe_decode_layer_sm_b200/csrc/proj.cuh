@@ -79,13 +79,6 @@ __global__ void pack_proj_groups_kernel(const T* __restrict__ src, T* __restrict
   }
 }
 
-// D = A B, from zero
-__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
-
 // a lane's eight scales of a group: outputs g and g + 8 of each tile
 template <int SC>
 struct ScaleRegs {
@@ -245,6 +238,86 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
                      : __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(p.x) + at + i));
       }
     };
+    // chunk q (8 inputs) of a row, scaled, to its place; the sum of a block's 32 inputs
+    auto put = [&](int r, int q, bool there, const float* v, float up) {
+      float sum = 0.f;
+      if (there) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float a = v[2 * j] * up, b = v[2 * j + 1] * up;
+          hi[j] = pack_h2(a, b);
+          const __half2 hh = *reinterpret_cast<const __half2*>(&hi[j]);
+          lo[j] = F32 ? pack_h2(a - __low2float(hh), b - __high2float(hh)) : 0u;
+          const __half2 ll = *reinterpret_cast<const __half2*>(&lo[j]);
+          sum += __low2float(hh) + __high2float(hh);
+          if (F32) sum += __low2float(ll) + __high2float(ll);
+        }
+        const int at = ((w0 + (q >> 2)) * R + r) * 4 + (q & 3);
+        xs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (F32) xs[(size_t)kb_max * R * 4 + at] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      if (!MX) {
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+        if (there && t == 0) xsum[(w0 + (q >> 2)) * 8 + r] = sum;
+      }
+    };
+    // the power of two that takes a row's largest magnitude to [2^14, 2^15); its inverse is kept
+    auto scale_row = [&](int r, float most) {
+      most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
+      int e = 14 - ((int)(__float_as_uint(most) >> 23) - 127);
+      e = most > 0.f && most <= 3.402823466e38f ? min(e, 100) : 0;
+      if (lane == 0 && r < R) unscale[kw * 8 + r] = __uint_as_float((uint32_t)(127 - e) << 23);
+      return __uint_as_float((uint32_t)(e + 127) << 23);
+    };
+    // A part that fits registers: all its loads in flight at once (8 rows of
+    // 5120 inputs: 20 us where the loop below reads each row twice, 12 so)
+    auto convert_held = [&](auto rows) {
+      constexpr int kRows = decltype(rows)::value;
+      for (int r0 = team; r0 < R; r0 += kRows * teams) {
+        uint4 raw[kRows][2][F32 ? 2 : 1];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int r = r0 + i * teams, q = lane + 32 * k;
+#pragma unroll
+            for (int c = 0; c < (F32 ? 2 : 1); ++c) {
+              raw[i][k][c] = make_uint4(0u, 0u, 0u, 0u);
+              if (r < R && q < wn * 4)
+                raw[i][k][c] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(p.x) +
+                                                                    ((long long)r * p.x_row + row0 + q * 8) * (F32 ? 4 : 2)) + c);
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int r = r0 + i * teams;
+          if (r >= R) break;
+          float v[2][8];
+          float most = 0.f;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint4 a = raw[i][k][0];
+            if (F32) {
+              const uint4 b = raw[i][k][F32 ? 1 : 0];
+              const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[k][j] = __uint_as_float(w[j]);
+            } else {
+              const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) v[k][2 * j] = bf16lo(w[j]), v[k][2 * j + 1] = bf16hi(w[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[k][j]));
+          }
+          const float up = scale_row(r, most);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) put(r, lane + 32 * k, lane + 32 * k < wn * 4, v[k], up);
+        }
+      }
+    };
     // kRows: rows whose loads are in flight together
     auto convert = [&](auto vec, auto rows) {
       constexpr int kRows = decltype(rows)::value;
@@ -264,52 +337,23 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
             }
           }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-#pragma unroll
-          for (int o = 16; o; o >>= 1) amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xFFFFFFFFu, amax[i], o));
-          // 2^e takes the largest magnitude to [2^14, 2^15)
-          int e = 14 - ((int)(__float_as_uint(amax[i]) >> 23) - 127);
-          e = amax[i] > 0.f && amax[i] <= 3.402823466e38f ? min(e, 100) : 0;
-          if (lane == 0 && r0 + i * teams < R)
-            unscale[kw * 8 + r0 + i * teams] = __uint_as_float((uint32_t)(127 - e) << 23);
-          amax[i] = __uint_as_float((uint32_t)(e + 127) << 23);
-        }
+        for (int i = 0; i < kRows; ++i) amax[i] = scale_row(r0 + i * teams, amax[i]);
         for (int q0 = 0; q0 < wn * 4; q0 += 32) {
           const int q = q0 + lane;
 #pragma unroll
           for (int i = 0; i < kRows; ++i) {
             const int r = r0 + i * teams;
             if (r < R) {
-              float sum = 0.f;
-              if (q < wn * 4) {
-                float v[8];
-                get8(vec, r, q, v);
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const float a = v[2 * j] * amax[i], b = v[2 * j + 1] * amax[i];
-                  hi[j] = pack_h2(a, b);
-                  const __half2 hh = *reinterpret_cast<const __half2*>(&hi[j]);
-                  lo[j] = F32 ? pack_h2(a - __low2float(hh), b - __high2float(hh)) : 0u;
-                  const __half2 ll = *reinterpret_cast<const __half2*>(&lo[j]);
-                  sum += __low2float(hh) + __high2float(hh);
-                  if (F32) sum += __low2float(ll) + __high2float(ll);
-                }
-                const int at = ((w0 + (q >> 2)) * R + r) * 4 + (q & 3);
-                xs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if (F32) xs[(size_t)kb_max * R * 4 + at] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-              }
-              if (!MX) {
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-                if (q < wn * 4 && t == 0) xsum[(w0 + (q >> 2)) * 8 + r] = sum;
-              }
+              float v[8];
+              if (q < wn * 4) get8(vec, r, q, v);
+              put(r, q, q < wn * 4, v, amax[i]);
             }
           }
         }
       }
     };
-    if (p.x_vec) convert(std::true_type{}, std::integral_constant<int, 4>{});
+    if (p.x_vec && wn <= 16) convert_held(std::integral_constant<int, F32 ? 4 : 8>{});
+    else if (p.x_vec) convert(std::true_type{}, std::integral_constant<int, 4>{});
     else convert(std::false_type{}, std::integral_constant<int, 1>{});
     if (teams > 1) __syncthreads();
     else __syncwarp();
