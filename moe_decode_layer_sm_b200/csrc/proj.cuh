@@ -145,10 +145,10 @@ size_t proj_smem(int rows, int kb) {
 // fixed order, then the cluster's, pushed to the CTA that writes the output:
 // no scratch, no atomics.
 //
-// Measured: 131072 x 5120 MXFP4, 8 rows, 77 us (4.6 TB/s; the pair converter
+// Measured: 131072 x 5120 MXFP4, 8 rows, 76 us (4.7 TB/s; the pair converter
 // and the scales keep the integer pipe busy, 158 instructions for 2048 codes);
-// 7168 x 5120 int4, 1 row, 9.8 us (2.4 until x is ready, 3.7 of weights at
-// 5.1 TB/s on the 112 SMs that have an output block).
+// 7168 x 5120 int4, 1 row 8.5 us, 8 rows 12 (the launch, x, 3.7 us of weights at
+// 5.1 TB/s on the 112 SMs that have an output block, the sums).
 template <bool F32, int SC, bool ZP>
 __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_constant__ ProjParams p) {
   namespace cg = cooperative_groups;
@@ -271,8 +271,9 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
       if (lane == 0 && r < R) unscale[kw * 8 + r] = __uint_as_float((uint32_t)(127 - e) << 23);
       return __uint_as_float((uint32_t)(e + 127) << 23);
     };
-    // A part that fits registers: all its loads in flight at once (8 rows of
-    // 5120 inputs: 20 us where the loop below reads each row twice, 12 so)
+    // A part that fits registers: all its loads in flight at once (7168 x 5120,
+    // 8 rows: 20 us where the loop below reads each row twice, 12 so).  Eight
+    // rows at a time cost the MXFP4 kernel's loop registers and 4 %.
     auto convert_held = [&](auto rows) {
       constexpr int kRows = decltype(rows)::value;
       for (int r0 = team; r0 < R; r0 += kRows * teams) {
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
         }
       }
     };
-    if (p.x_vec && wn <= 16) convert_held(std::integral_constant<int, F32 ? 4 : 8>{});
+    if (p.x_vec && wn <= 16) convert_held(std::integral_constant<int, F32 || MX ? 4 : 8>{});
     else if (p.x_vec) convert(std::true_type{}, std::integral_constant<int, 4>{});
     else convert(std::false_type{}, std::integral_constant<int, 1>{});
     if (teams > 1) __syncthreads();
