@@ -71,9 +71,10 @@ __device__ __forceinline__ bool fp8_near_border(float q) {
 // which the exact quotient lies, or onto it.  The border has 5 bits, so the
 // sign of x - border x s is exact.  A q that lies beyond a code ends next to
 // that code's other border, on the side of the code.  low: 2^-6 where |q| is
-// below it (codes are as far apart there as above), else 0.
+// below it (codes are as far apart there as above), else 0; their sum is cut,
+// so that it stays below 2^-5, where codes lie further apart.
 __device__ __forceinline__ float fp8_place(float q, float x, float s, float low) {
-  const float b = __uint_as_float((__float_as_uint(fabsf(q) + low) & 0xFFF00000u) | 0x80000u) - low;
+  const float b = __uint_as_float((__float_as_uint(__fadd_rz(fabsf(q), low)) & 0xFFF00000u) | 0x80000u) - low;
   const int r = __float_as_int(fmaf(-b, s, fabsf(x)));
   return __uint_as_float((__float_as_uint(b) + min(max(r, -1), 1)) | (__float_as_uint(q) & 0x80000000u));
 }

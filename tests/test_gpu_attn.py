@@ -256,6 +256,23 @@ def test_append_strides_alignment_and_values(m):
     check_append(m, "f32", [13], [13], 16, 8, 64, 16, None, k=v, v=v.flip(1))
 
 
+def test_append_codes_and_borders_between_them(m):
+    """Values that lie exactly on codes and on borders, and next to them, at many
+    scales: the quotient's own rounding must not move one."""
+    g = gen(190)
+    heads = 64
+    s = torch.randint(1 << 12, 1 << 13, (heads,), device="cuda", generator=g).double() * 2.0 ** -20   # 13 bits: exact products
+    n = torch.arange(16 * 64, device="cuda")
+    steps = torch.cat([n[:600], torch.randint(0, 448 * 1024, (16 * 64 - 600,), device="cuda", generator=g) & ~0x1FF])
+    v = (s[:, None] * (steps.double() * 2.0 ** -10)).float()
+    assert torch.equal(v.double(), s[:, None] * (steps.double() * 2.0 ** -10))
+    v = torch.where(n % 3 == 0, v, torch.where(n % 3 == 1, torch.nextafter(v, v + 1), torch.nextafter(v, v - 1)))
+    v = torch.where(n % 2 == 0, v, -v)
+    v[:, 777] = 448.0 * s.float()
+    v = v.view(heads, 16, 64).transpose(0, 1)[None].contiguous()
+    check_append(m, "f32", [16], [16], 16, heads, 64, 16, None, k=v, v=v.flip(1))
+
+
 def test_append_token_by_token_keeps_the_page(m):
     """A page filled in many calls: the scale grows with the values, the older
     codes follow, and the slots behind the sequence keep their bytes."""
