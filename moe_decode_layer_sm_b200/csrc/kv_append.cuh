@@ -57,6 +57,12 @@ __device__ __forceinline__ float fp8_sticky(double q) {
   return (double)f != q && fabsf(f) < kFp8Max ? __uint_as_float(__float_as_uint(f) | 1u) : f;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // whether q, a quotient that is off by less than 4 units in the last place,
 // may lie on the other side of a border between two codes: halfway between two
 // mantissas of 3 bits.  Below 2^-6 the codes are as far apart as above it.
@@ -72,7 +78,8 @@ __device__ __forceinline__ bool fp8_near_border(float q) {
 // sign of x - border x s is exact.  A q that lies beyond a code ends next to
 // that code's other border, on the side of the code.  low: 2^-6 where |q| is
 // below it (codes are as far apart there as above), else 0; their sum is cut,
-// so that it stays below 2^-5, where codes lie further apart.
+// so that it stays below 2^-5, where codes lie further apart.  x is a number:
+// of NaN the step by bits would make a zero.
 __device__ __forceinline__ float fp8_place(float q, float x, float s, float low) {
   const float b = __uint_as_float((__float_as_uint(__fadd_rz(fabsf(q), low)) & 0xFFF00000u) | 0x80000u) - low;
   const int r = __float_as_int(fmaf(-b, s, fabsf(x)));
@@ -321,7 +328,7 @@ __global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kern
       cp_async_wait<kHeads - 1>();
       float val[U][16];
       double amax = 0.0;
-      float top = 0.f;   // of the values that are not rotated
+      float top = 0.f;   // of the values that are not rotated; NaN if one of them is
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (live[u]) {
@@ -368,7 +375,7 @@ __global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kern
                     amax = fmax(amax, fabs(y));
                     x = (float)y;
                   } else {
-                    top = fmaxf(top, fabsf(x));
+                    top = max_nan(top, fabsf(x));
                   }
                   val[u][8 * v + i] = x;
                 }
@@ -380,11 +387,11 @@ __global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kern
       if (PLAIN) {
         amax = __uint_as_float(block_max(__float_as_uint(top)));
       } else {
-        amax = fmax(amax, (double)top);
+        amax = top == top ? fmax(amax, (double)top) : (double)top;
         amax = __longlong_as_double((long long)block_max((unsigned long long)__double_as_longlong(amax)));
       }
-      const bool infinite = !(amax < 1e300);
-      if (infinite) {   // an infinity among them: once more, without
+      const bool special = !(amax < 1e300);   // (the bits of NaN order above infinity's)
+      if (special) {   // an infinity or NaN among them: once more, without
         amax = 0.0;
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kern
                        1.175494351e-38f);
       if (older > 0) sc = fmaxf(sc, was);
       const float rs = rcp_approx(sc);
-      const bool exact = infinite || sc < 1e-27f;   // fp8_place does not hold
+      const bool exact = special || sc < 1e-27f;   // fp8_place does not hold
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (live[u]) {
