@@ -160,7 +160,8 @@ int mono_attn_plan(const mono_attn_config* cfg, mono_attn_plan_t** out);
  * NULL) and values to its pages.  Per touched page and head, over the new
  * tokens' finite values:
  *   s' = max(amax / 448, 2^-126), and not below the page's scale s when the
- *        page holds older tokens of the sequence (position below the first new one)
+ *        page holds older tokens of the sequence (position below the first new one);
+ *        NaN if that scale is, and then so are the new codes
  *   code = e4m3(x / s'), nearest, ties to even, saturating (infinities too); NaN stays NaN
  *        (the rotated key x in binary64: codes are rounded once)
  *   older codes become e4m3(code s / s') where s' > s

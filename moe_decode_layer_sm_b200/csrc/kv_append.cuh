@@ -405,9 +405,9 @@ __global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kern
       const float af = (float)amax, q0 = af * (1.f / kFp8Max);
       float sc = fmaxf(PLAIN ? fmaf(fmaf(-q0, kFp8Max, af), 1.f / kFp8Max, q0) : (float)(amax * (1.0 / (double)kFp8Max)),
                        1.175494351e-38f);
-      if (older > 0) sc = fmaxf(sc, was);
+      if (older > 0) sc = max_nan(sc, was);   // a page whose older values are none has none
       const float rs = rcp_approx(sc);
-      const bool exact = special || sc < 1e-27f;   // fp8_place does not hold
+      const bool exact = special || !(sc >= 1e-27f);   // fp8_place does not hold
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (live[u]) {

@@ -44,3 +44,23 @@ def test_append_nan_stays_nan(m, dtype, rot, d, page):
         x[0, page - 1, 1, d - 1], x[0, 0, 1, 40] = -math.nan, math.nan
         x[0, :, 2] = math.nan
     check_append(m, dtype, [page], [page], page, 4, d, page, rope, k=k, v=v)
+
+
+def test_append_keeps_a_page_scale_that_is_nan(m):
+    """The older codes of such a page are no numbers, and stay none."""
+    d, page, heads = 64, 16, 3
+    for dtype in ("bf16", "f32"):
+        cache = make_cache(m, 3, heads, page, d, 310)
+        cache.k_scale[1, 1], cache.v_scale[1, 2] = math.nan, math.nan
+        before = {n: getattr(cache, n).clone() for n in ("k", "v")}
+        k, v = (normal((1, 3, heads, d), DT[dtype], 311 + i) for i in (0, 1))
+        plan = m.AttnPlan(heads, heads, d, page, 3, 1, 2, max_new=3, dtype=dtype)
+        want = R.append(cache, k, v, [9], [[1, 2]], [3], None, page)
+        plan.append(cache, k, v, i32([9]), i32([[1, 2]]))
+        for name, bad in (("k", 1), ("v", 2)):
+            code, scale = getattr(cache, name), getattr(cache, name + "_scale")
+            assert math.isnan(scale[1, bad].item())
+            assert torch.isnan(code[1, bad, 6:9].float()).all()
+            assert torch.equal(bits(code)[1, bad, :6], bits(before[name])[1, bad, :6])
+            for h in set(range(heads)) - {bad}:
+                assert torch.equal(code[1, h].double(), want[name][1, h]) and scale[1, h] == want[name + "_scale"][1, h]
