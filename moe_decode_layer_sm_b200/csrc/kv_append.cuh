@@ -407,7 +407,9 @@ __global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kern
                        1.175494351e-38f);
       if (older > 0) sc = max_nan(sc, was);   // a page whose older values are none has none
       const float rs = rcp_approx(sc);
-      const bool exact = special || !(sc >= 1e-27f);   // fp8_place does not hold
+      // where fp8_place does not hold; and there a rotated value's fp32 form is not
+      // good enough: beyond fp32's range, or among its subnormals
+      const bool exact = special || !(sc >= 1e-27f) || !(af <= 3.402823466e38f);
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (live[u]) {
@@ -424,6 +426,8 @@ __global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kern
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 y[i] = fp8_place(y[i], val[u][8 * v + i], sc, fabsf(y[i]) < 0.015625f ? 0.015625f : 0.f);
+            } else if (turned && exact) {
+              near = amax > 0.0 ? 0xFFu : 0u;
             } else {
 #pragma unroll
               for (int i = 0; i < 8; ++i)

@@ -64,3 +64,36 @@ def test_append_keeps_a_page_scale_that_is_nan(m):
             assert torch.equal(bits(code)[1, bad, :6], bits(before[name])[1, bad, :6])
             for h in set(range(heads)) - {bad}:
                 assert torch.equal(code[1, h].double(), want[name][1, h]) and scale[1, h] == want[name + "_scale"][1, h]
+
+
+def check_rotated_keys(m, k, rot, il=False):
+    """One page of fp32 keys, its codes and scales from the rotated keys in fp64."""
+    _, page, heads, d = k.shape
+    rope = m.Rope(rot, interleaved=il)
+    plan = m.AttnPlan(heads, heads, d, page, 1, 1, 1, max_new=1, dtype="f32")
+    cache = m.KVCache.empty(1, heads, page, d)
+    plan.append(cache, k, k, i32([page]), i32([[0]]), rope=rope)
+    y = R.rotate(k[0], torch.arange(page, device="cuda"), rope).transpose(0, 1)
+    finite = torch.where(torch.isfinite(y), y.abs(), 0.0)
+    scale = (finite.amax((1, 2)) / 448).float().clamp_min(2.0 ** -126)
+    assert torch.equal(cache.k_scale[0], scale)
+    want = R.nearest_fp8(y / scale.double()[:, None, None])
+    got = cache.k[0].double()
+    assert ((got == want) | (torch.isnan(got) & torch.isnan(want))).all(), (got != want).sum().item()
+
+
+@pytest.mark.parametrize("rot,il", [(64, False), (64, True), (32, False), (10, False)])
+def test_append_rotated_keys_at_the_ends_of_the_range(m, rot, il):
+    """Rotated keys that lie beyond the largest fp32 number, which the inputs do
+    not, and keys among the smallest, whose codes are of scale 2^-126."""
+    page, d = 16, 64
+    g = gen(320)
+    big = (torch.rand((1, page, 8, d), device="cuda", generator=g) * 0.5 + 0.5) * 3.4e38
+    check_rotated_keys(m, big, rot, il)
+    big[0, 3, 2, 1] = math.inf
+    check_rotated_keys(m, big, rot, il)
+    tiny = ((torch.rand((1, page, 1024, d), device="cuda", generator=g, dtype=torch.float64) - 0.5) * 2.0 ** -126).float()
+    check_rotated_keys(m, tiny, rot, il)
+    tiny[0, :, 5] = 0
+    tiny[0, 2, 7, 3] = math.inf
+    check_rotated_keys(m, tiny[:, :, :16].contiguous(), rot, il)
