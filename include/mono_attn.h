@@ -125,7 +125,8 @@ typedef struct {
  *         (and, with a window, before its first visible token) may hold anything.
  * A page id outside [0, num_pages), lens above max_pages x page_size or below
  * 0, or n_new above width is recorded for mono_attn_query_error; the tokens
- * concerned are left out and nothing outside the buffers is touched. */
+ * concerned are left out (with n_new above width the whole sequence: its pages
+ * and its rows stay as they were) and nothing outside the buffers is touched. */
 typedef struct {
   int seqs;
   int width;

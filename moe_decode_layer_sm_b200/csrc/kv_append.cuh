@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(append_threads(U), U == 4 ? 1 : 3) append_kern
   const SeqView sv = view_seq(__ldg(p.lens + s), n_new, p.width, cap);
   const bool reporter = threadIdx.x == 0 && blockIdx.y == 0;
   if (sv.bad && reporter && blockIdx.x == 0) record_bad(p.bad, sv.bad, s, sv.bad_value);
+  if (sv.left_out) return;
   // tokens [a, b) of this page
   const int first = max(sv.first, 0);
   const int page_no = (first >> p.page_shift) + blockIdx.x;

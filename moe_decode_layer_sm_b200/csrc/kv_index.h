@@ -15,19 +15,21 @@ namespace mono {
 enum { kBadPage = 1, kBadLen = 2, kBadNew = 3 };
 
 // A sequence of a call: its live rows, the position of the first of them
-// (below zero where the sequence is shorter than its new tokens) and what was
-// wrong with its entries (0 or kBad*).
+// (below zero where the sequence is shorter than its new tokens), what was
+// wrong with its entries (0 or kBad*), and whether it is left out: with more new
+// tokens than rows, row j's position is not that of a token the caller gave.
 struct SeqView {
   int n, first, bad, bad_value;
+  bool left_out;
 };
 
 MONO_HD SeqView view_seq(int len, int n_new, int width, int cap) {
-  SeqView v{n_new, 0, 0, 0};
+  SeqView v{n_new, 0, 0, 0, n_new > width};
   if (v.n <= 0) {
     v.n = 0;
     return v;
   }
-  if (v.n > width) {
+  if (v.left_out) {
     v.n = width;
     v.bad = kBadNew;
     v.bad_value = n_new;
@@ -62,7 +64,7 @@ MONO_HD long long code_row(int page, int kv_heads, int h, int page_size, int tok
 // of `tile` tokens that its rows read; at least one tile for a live sequence,
 // whose rows have to be written even if they see nothing
 MONO_HD int seq_tiles(const SeqView& v, int window, int cap, int tile, int lead) {
-  if (v.n == 0) return 0;
+  if (v.n == 0 || v.left_out) return 0;
   const int lo = row_lo(v, 0, window), hi = row_hi(v, v.n - 1, cap);
   if (hi <= lo) return lead + 1;
   return lead + (hi - 1) / tile - lo / tile + 1;

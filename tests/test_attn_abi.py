@@ -288,3 +288,11 @@ def test_equal_runs_cover_the_line_and_keep_their_slots(idx):
                     assert slot // 2 == c and slot not in used
                     used.add(slot)
             base += n
+
+
+def test_more_new_tokens_than_rows_have_no_work(idx):
+    """Such a sequence is left out: no tile of it, whatever else is wrong."""
+    for length in (-1, 0, 50, 1024, 1025):
+        for lead in (0, 3):
+            assert idx.tiles(length, 9, 8, 1024, 0, 32, lead) == 0
+            assert idx.tiles(length, 8, 8, 1024, 0, 32, lead) > lead

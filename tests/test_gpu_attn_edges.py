@@ -97,3 +97,31 @@ def test_append_rotated_keys_at_the_ends_of_the_range(m, rot, il):
     tiny[0, :, 5] = 0
     tiny[0, 2, 7, 3] = math.inf
     check_rotated_keys(m, tiny[:, :, :16].contiguous(), rot, il)
+
+
+# ------------------------------------------------------ entries out of range
+
+@pytest.mark.parametrize("lens", [(20, 9), (20, 70)])
+def test_more_new_tokens_than_rows_leave_a_sequence_out(m, lens):
+    """Where row 0 would lie is not known to the caller's rows: nothing of the
+    sequence is written, its rows stay, and the other sequence is served."""
+    d, page, hk, hq = 64, 16, 2, 4
+    cache = make_cache(m, 5, hk, page, d, 330)
+    k, v = (normal((2, 2, hk, d), torch.bfloat16, 331 + i) for i in (0, 1))
+    plan = m.AttnPlan(hq, hk, d, page, 5, 2, 4, max_new=2)
+    table = [[0, 1, -1, -1], [2, 3, 4, -1]]
+    want = R.append(cache, k, v, [lens[0], 0], table, [2, 0], None, page)
+    plan.append(cache, k, v, i32(lens), i32(table), n_new=i32([2, 5]))
+    assert plan.query_error()[0] == -9
+    for n in ("k", "v"):
+        assert torch.equal(getattr(cache, n).double(), want[n])
+        assert torch.equal(getattr(cache, n + "_scale"), want[n + "_scale"])
+    q = normal((2, 2, hq, d), torch.bfloat16, 333)
+    out, lse = torch.full_like(q, 5.0), torch.full((2, 2, hq), 5.0, device="cuda")
+    plan.attend(cache, q, i32(lens), i32(table), out, lse=lse, n_new=i32([2, 5]))
+    rc, st = plan.query_error()
+    assert (rc, st.seq) == (-9, 1)
+    assert (out[1] == 5.0).all() and (lse[1] == 5.0).all()
+    wo, wl, ob, lb = R.attend(cache, q, [lens[0], 0], table, [2, 0], page, 1 / math.sqrt(d))
+    within(out[0], wo[0], ob[0])
+    within(lse[0], wl[0], lb[0])
