@@ -371,7 +371,6 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
     find_pages(1, pid[1]);
     QRows<D> q;
     load_q(warp, q);
-    uint32_t vref = 0u;   // as bits
 
     float rf[NT][2];
     float O[D / 16][NT][4], mx[NT][2], l[NT][2];
@@ -529,15 +528,10 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
       if (i >= 0) {
         cp_async_wait<2 * kStages - 1>();
         __syncwarp();
-        // values enter in units of vref, a power of two not below any of their scales so far
         float vsc[kSubs];
-        uint32_t vtop = 0u;
 #pragma unroll
-        for (int b = 0; b < kSubs; ++b) vsc[b] = (ok[0] >> b) & 1u ? sc[4 + b] : 0.f, vtop = max(vtop, __float_as_uint(vsc[b]));
-        vtop = (vtop + 0x7FFFFFu) & 0x7F800000u;
-        if (__any_sync(0xFFFFFFFFu, grew) || vtop > vref) {
-          const float down = vtop > vref ? __uint_as_float(vref) * __uint_as_float(0x7F000000u - vtop) : 1.f;
-          vref = max(vref, vtop);
+        for (int b = 0; b < kSubs; ++b) vsc[b] = (ok[0] >> b) & 1u ? sc[4 + b] : 0.f;
+        if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -547,10 +541,9 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
               mx[n][r] = now;
               l[n][r] *= keep;
 #pragma unroll
-              for (int w = 0; w < D / 16; ++w) O[w][n][r] *= keep * down, O[w][n][2 + r] *= keep * down;
+              for (int w = 0; w < D / 16; ++w) O[w][n][r] *= keep, O[w][n][2 + r] *= keep;
             }
         }
-        const float vinv = vref ? __uint_as_float(0x7F000000u - vref) : 0.f;
         uint32_t pf[kSubs][NT][kSplit][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -558,13 +551,16 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
           const float off1 = mx[n][1] == -INFINITY ? 0.f : mx[n][1] - kPBias;
 #pragma unroll
           for (int b = 0; b < kSubs; ++b) {
-            const float r = vsc[b] * vinv;
             float e[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               e[j] = exp2_approx(c[b][n][j] - (j & 1 ? off1 : off0));
               l[n][j & 1] += e[j];
-              e[j] *= r;
+            }
+            // a scale that is no finite number: only what sees the page's tokens meets it
+            if (!(fabsf(vsc[b]) <= 3.402823466e38f)) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) e[j] = c[b][n][j] == -INFINITY ? 0.f : e[j] * vsc[b];
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -577,9 +573,13 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
             }
           }
         }
-        // output, 16 tokens at a time
+        // output, 16 tokens of a page at a time: their products by the matrix unit,
+        // which cuts what it adds up, then times the page's scale in fp32.  With
+        // the scale in the probabilities instead, a page of large values took the
+        // others' bits, also from rows that do not see it.
 #pragma unroll
         for (int b = 0; b < kSubs; ++b) {
+          if (!(fabsf(vsc[b]) <= 3.402823466e38f)) vsc[b] = 1.f;
           uint32_t vw[4][S::kValWords];   // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -662,15 +662,11 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
             e4m3x4_to_h2(x1, a[2], a[3]);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              if (F32) {   // the matrix unit cuts what it adds up; fp32 rows round instead
-                float o[4];
-                mma_f16_first(o, a, pf[b][n][0][0], pf[b][n][0][1]);
-                mma_f16(o, a, pf[b][n][kSplit - 1][0], pf[b][n][kSplit - 1][1]);
+              float o[4];
+              mma_f16_first(o, a, pf[b][n][0][0], pf[b][n][0][1]);
+              if (F32) mma_f16(o, a, pf[b][n][kSplit - 1][0], pf[b][n][kSplit - 1][1]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) O[w][n][j] += o[j];
-              } else {
-                mma_f16(O[w][n], a, pf[b][n][0][0], pf[b][n][0][1]);
-              }
+              for (int j = 0; j < 4; ++j) O[w][n][j] = fmaf(o[j], vsc[b], O[w][n][j]);
             }
           }
         }
@@ -686,7 +682,6 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
 
     // the CTA's warps together
     __syncthreads();   // q and the rings are read
-    const float vf = __uint_as_float(vref);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -701,7 +696,7 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
         for (int w = 0; w < S::kValWords; ++w) {
           const int d = D == 64 ? g * 8 + w * 4 : (w >> 2) * 128 + g * 16 + (w & 3) * 4;
           *reinterpret_cast<float4*>(merge + ((size_t)warp * kRows + row) * D + merge_place<D>(row, d)) =
-              make_float4(O[2 * w][n][r] * vf, O[2 * w][n][2 + r] * vf, O[2 * w + 1][n][r] * vf, O[2 * w + 1][n][2 + r] * vf);
+              make_float4(O[2 * w][n][r], O[2 * w][n][2 + r], O[2 * w + 1][n][r], O[2 * w + 1][n][2 + r]);
         }
       }
     __syncthreads();

@@ -125,3 +125,92 @@ def test_more_new_tokens_than_rows_leave_a_sequence_out(m, lens):
     wo, wl, ob, lb = R.attend(cache, q, [lens[0], 0], table, [2, 0], page, 1 / math.sqrt(d))
     within(out[0], wo[0], ob[0])
     within(lse[0], wl[0], lb[0])
+
+
+# ------------------------------------------------------------------ attention
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (64, 24, 2), (128, 10, 2), (128, 24, 2), (256, 4, 2)])
+@pytest.mark.parametrize("power", [24, 40, 90, -90])
+def test_attend_page_that_other_rows_see(m, dtype, d, hq, hk, power):
+    """A page of values far larger (or smaller) than the others, of which only
+    the first of four rows sees a token: the other rows keep all their bits."""
+    page, window, lens = 16, 20, [38]
+    cache = make_cache(m, 4, hk, page, d, 340)
+    table = [[2, 0, 3]]
+    cache.v_scale[2] *= 2.0 ** power
+    q = normal((1, 4, hq, d), DT[dtype], 341)
+    plan = m.AttnPlan(hq, hk, d, page, 4, 1, 3, max_new=4, dtype=dtype, window=window)
+    out = plan.attend(cache, q, i32(lens), i32(table), torch.empty_like(q))
+    want, _, ob, _ = R.attend(cache, q, lens, table, [4], page, 1 / math.sqrt(d), window)
+    within(out[:, 1:], want[:, 1:], ob[:, 1:])
+    if power < 0:   # row 0's bound counts the largest value that it sees, which is one of the others here
+        within(out, want, ob)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,hq,hk,seqs,length", [(64, 4, 2, 1, 100), (128, 5, 1, 1, 9000), (64, 8, 4, 64, 1000),
+                                                 (64, 64, 4, 50, 1000), (128, 10, 2, 100, 600), (256, 4, 2, 90, 500)])
+@pytest.mark.parametrize("power", [24, 40, 90])
+def test_attend_large_page_without_weight(m, dtype, d, hq, hk, seqs, length, power):
+    """A page of values 2^power times as large whose tokens have no weight (logits
+    200 below the others: exp(-200) 2^90 is 1e-60): the others keep their bits.
+    The bound is that of a cache where the page holds zeros.  Many sequences: a
+    warp goes on to other pages of the item."""
+    page = 64
+    per = -(-length // page)
+    pages = per * seqs
+    cache = make_cache(m, pages, hk, page, d, 350)
+    q = normal((seqs, 1, hq, d), DT[dtype], 351)
+    q[..., 0] = 8.0   # every row's first element; the large page's keys hold all they have there
+    code = torch.zeros(d, device="cuda")
+    code[0] = -448.0
+    large = range(1, pages, per)   # the second page of each sequence
+    for i in large:
+        cache.k[i] = code.to(R.FP8)
+        cache.k_scale[i] = 230 * math.sqrt(d) / (8 * 448)
+        cache.v_scale[i] *= 2.0 ** power
+    table = [list(range(s * per, (s + 1) * per)) for s in range(seqs)]
+    plan = m.AttnPlan(hq, hk, d, page, pages, seqs, per, dtype=dtype)
+    out = plan.attend(cache, q, i32([length] * seqs), i32(table), torch.empty_like(q))
+    for i in large:
+        cache.v[i] = torch.zeros(d, device="cuda").to(R.FP8)
+    want, _, ob, _ = R.attend(cache, q, [length] * seqs, table, [1] * seqs, page, 1 / math.sqrt(d))
+    within(out, want, ob)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attend_one_token_gives_its_value(m, dtype):
+    """Its probability is 1: the value is rounded once, to the nearest.  Twice the
+    argument's rounding, (|logit| + 24) 2^-23 with logits below 8, lies between
+    the sum and the probability: 2^-17."""
+    for d, hq, hk in ((64, 8, 8), (128, 40, 8), (256, 16, 8)):
+        cache = make_cache(m, 1, hk, 64, d, 360)
+        q = normal((1, 1, hq, d), DT[dtype], 361) * 0.25
+        plan = m.AttnPlan(hq, hk, d, 64, 1, 1, 1, dtype=dtype)
+        out = plan.attend(cache, q, i32([1]), i32([[0]]), torch.empty_like(q))
+        v = (cache.v[0, :, 0].double() * cache.v_scale[0].double()[:, None]).repeat_interleave(hq // hk, 0)
+        unit = torch.exp2(torch.floor(torch.log2(v.abs().clamp_min(2.0 ** -100)))) * torch.finfo(DT[dtype]).eps
+        assert ((out[0, 0].double() - v).abs() <= unit / 2 + v.abs() * 2.0 ** -17).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 24, 2), (256, 4, 2)])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("scale", [math.nan, math.inf])
+def test_attend_scale_that_is_no_number(m, dtype, d, hq, hk, which, scale):
+    """Rows that see none of the page stay clean; with NaN all that see it are NaN."""
+    page, lens, table = 16, [34], [[1, 3, 0]]   # rows 0 and 1 end at token 31
+    cache, clean = (make_cache(m, 4, hk, page, d, 370) for _ in range(2))
+    getattr(cache, which + "_scale")[0, 1] = scale
+    q = normal((1, 4, hq, d), DT[dtype], 371)
+    plan = m.AttnPlan(hq, hk, d, page, 4, 1, 3, max_new=4, dtype=dtype)
+    out = plan.attend(cache, q, i32(lens), i32(table), torch.empty_like(q))
+    want, _, ob, _ = R.attend(clean, q, lens, table, [4], page, 1 / math.sqrt(d))
+    half = hq // hk
+    within(out[:, :2], want[:, :2], ob[:, :2])
+    within(out[:, :, :half], want[:, :, :half], ob[:, :, :half])
+    if math.isnan(scale):
+        assert torch.isnan(out[:, 2:, half:]).all()
+    elif which == "v":
+        assert not torch.isfinite(out[:, 2:, half:]).any()
