@@ -185,7 +185,9 @@ int mono_attn_append(mono_attn_plan_t* plan, const mono_kv_cache* cache, const m
  * Sums and softmax statistics are fp32; probabilities enter the products with
  * 11 bits (MONO_F32: 22) down to 2^-29 of the row's largest, below it in steps
  * of 2^-39.  q enters with 11 bits (MONO_F32: 22) of fp16's range below each
- * row's largest; rows whose largest is below 2^-86 keep fewer. */
+ * row's largest; rows whose largest is below 2^-86 keep fewer.  Values may have
+ * any magnitude for which the sum of exp(logit - largest) |v| stays below fp32's
+ * end; MONO_BF16 takes page scales below 2^-111 in steps of 2^-134. */
 int mono_attn_attend(mono_attn_plan_t* plan, const mono_kv_cache* cache, const mono_seqs* seqs, const mono_rows* q,
                      const mono_rows* out, float* lse, void* stream);
 

@@ -70,7 +70,8 @@ struct AttendParams {
 
 constexpr int kQRows = 2;         // rows of q that a warp loads together
 constexpr int kStages = 2;        // tiles that a warp has in flight or in use
-constexpr float kPBias = 15.f;   // probabilities are held as 2^15 p: fp16 keeps 11 bits down to p = 2^-29
+constexpr float kPBias = 15.f;   // probabilities are held as 2^15 p: fp16 keeps 11 bits down to p = 2^-29;
+constexpr float kPUnit = 1.f / 32768.f;   // sums of p times values come without it, or values above 2^113 would pass fp32's end
 
 template <int D, int NT, bool F32, int W>
 struct AttendShape {
@@ -126,7 +127,7 @@ struct Item {
 template <bool F32>
 __device__ __noinline__ void finish_row(const AttendParams& p, const Item& it, int r, int d, float4 o, float m, float l) {
   const int row = it.first + r, j = row / p.group, hq = it.h * p.group + (row - j * p.group);
-  const float inv = l > 0.f || l != l ? __fdiv_rn(1.f, l) : 0.f;
+  const float inv = l > 0.f || l != l ? __fdiv_rn(1.f / kPUnit, l) : 0.f;
   o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
   const long long at = (long long)it.s * p.o_seq + (long long)j * p.o_tok + (long long)hq * p.o_head + d;
   if (F32) {
@@ -580,6 +581,7 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
 #pragma unroll
         for (int b = 0; b < kSubs; ++b) {
           if (!(fabsf(vsc[b]) <= 3.402823466e38f)) vsc[b] = 1.f;
+          const float vs = F32 ? vsc[b] : vsc[b] * kPUnit;   // (inexact below 2^-111, where bf16 rows keep at least 8 bits)
           uint32_t vw[4][S::kValWords];   // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
               mma_f16_first(o, a, pf[b][n][0][0], pf[b][n][0][1]);
               if (F32) mma_f16(o, a, pf[b][n][kSplit - 1][0], pf[b][n][kSplit - 1][1]);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) O[w][n][j] = fmaf(o[j], vsc[b], O[w][n][j]);
+              for (int j = 0; j < 4; ++j) O[w][n][j] = fmaf(F32 ? o[j] * kPUnit : o[j], vs, O[w][n][j]);
             }
           }
         }

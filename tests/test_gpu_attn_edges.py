@@ -214,3 +214,23 @@ def test_attend_scale_that_is_no_number(m, dtype, d, hq, hk, which, scale):
         assert torch.isnan(out[:, 2:, half:]).all()
     elif which == "v":
         assert not torch.isfinite(out[:, 2:, half:]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 24, 2), (256, 4, 2)])
+@pytest.mark.parametrize("length", [1, 200, 9000])
+@pytest.mark.parametrize("power", [112, -100])
+def test_attend_values_at_the_ends_of_the_range(m, dtype, d, hq, hk, length, power):
+    """Values up to 2^112 times the usual, whose sums over 9000 tokens fp32 still
+    holds, and far below the usual."""
+    page = 64
+    pages = -(-length // page)
+    cache = make_cache(m, pages, hk, page, d, 380)
+    for s in (cache.v_scale,):
+        s *= 2.0 ** power
+    q = normal((1, 1, hq, d), DT[dtype], 381)
+    table = [list(range(pages))]
+    plan = m.AttnPlan(hq, hk, d, page, pages, 1, pages, dtype=dtype)
+    out = plan.attend(cache, q, i32([length]), i32(table), torch.empty_like(q))
+    want, _, ob, _ = R.attend(cache, q, [length], table, [1], page, 1 / math.sqrt(d))
+    within(out, want, ob)
