@@ -111,6 +111,13 @@ __device__ __forceinline__ float e8m0_ends(float s) {   // 2^-127 and NaN
   return b == 0u ? __uint_as_float(0x00400000u) : b == 0x7F800000u ? __uint_as_float(0x7FC00000u) : s;
 }
 
+// (w & mask) | 0x64006400, in one instruction (as two: 7168 x 5120 int4, 1 row, 9.4 us; 7.9 so)
+__device__ __forceinline__ uint32_t under_1024(uint32_t w, uint32_t mask) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "r"(mask), "r"(0x64006400u));
+  return r;
+}
+
 template <int SC, bool ZP>
 __host__ __device__ constexpr int proj_slot() {   // bytes of a block in a warp's ring: codes, scales, zeros
   return 1024 + 64 * ScaleRegs<SC>::kBytes + (ZP ? 64 : 0);
@@ -120,7 +127,7 @@ __host__ __device__ constexpr int proj_slot() {   // bytes of a block in a warp'
 template <bool F32, int SC, bool ZP>
 size_t proj_smem(int rows, int kb) {
   return (size_t)kProjWarps * kProjDepth * proj_slot<SC, ZP>() + (size_t)kb * rows * 64 * (F32 ? 2 : 1) +
-         (SC == kScaleE8m0 ? 0 : (size_t)kb * 32) + (size_t)kProjWarps * (rows * kProjRedRow + 8) * 4 + 2 * 512 * 4;
+         (size_t)kProjWarps * (rows * kProjRedRow + 8) * 4 + 2 * 512 * 4;
 }
 
 // A cluster of CTAs cuts the inputs and the warps of a team cut a CTA's part
@@ -133,15 +140,13 @@ size_t proj_smem(int rows, int kb) {
 // x is converted once a CTA, each row of a warp's part scaled by a power of
 // two to fp16's range (fp32 as two terms).  Codes become exact fp16 operands:
 //   e2m1   by the pair converter
-//   int4   by masking: a code in the low bits of a half is the subnormal
-//          q 2^-24, one nibble further up q 2^-20, which the tensor cores
-//          take at full rate; the zero point comes off the group's sum,
-//          sum (q - z) x = sum q x - z sum x, with sum x found once
-// so an int4 code costs half a mask and no conversion.  The matrix unit aligns
-// its sums by the operands' exponents, of which a subnormal has the wrong one:
-// that is worth 1e-6 of the result (2e-7 with normal operands), below bf16's
-// rounding, so only bf16 rows take it; fp32 rows make q a normal number.  A group's scale
-// multiplies the fp32 sum of its products.  The warps' sums are added in a
+//   int4   q - z: masked under the exponent of 1024 a code is the half 1024 + q,
+//          one nibble further up 1024 + 16 q, from which one exact operation
+//          takes 1024 + z, or (with a 16th) 64 + z
+// A group's scale multiplies the fp32 sum of its products.  (int4 codes as they
+// lie, fp16 subnormals, save that operation, but then the zero point has to come
+// off the sums, sum q x - z sum x, which loses weights near it: codes that equal
+// their zero point gave 1e-6 of sum z |x| s for 0.)  The warps' sums are added in a
 // fixed order, then the cluster's, pushed to the CTA that writes the output:
 // no scratch, no atomics.
 //
@@ -164,8 +169,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
   const int kbs = kb1 - kb0, kb_max = (p.kblocks + cs - 1) >> p.cluster_log2, R = p.rows;
   unsigned char* ring = smem + (size_t)warp * kProjDepth * kSlot;
   uint4* xs = reinterpret_cast<uint4*>(smem + (size_t)kProjWarps * kProjDepth * kSlot);   // [split][kb][row][t] 8 halves
-  float* xsum = reinterpret_cast<float*>(xs + (size_t)kb_max * R * 4 * kSplit);           // [kb][8 rows], int4
-  float* unscale = xsum + (MX ? 0 : kb_max * 8);          // [kw][8 rows]
+  float* unscale = reinterpret_cast<float*>(xs + (size_t)kb_max * R * 4 * kSplit);        // [kw][8 rows]
   float* part = unscale + kProjWarps * 8;                 // [turn][rank][512 / cs]
   float* red = part + 2 * 512 + team * tw * R * kProjRedRow;   // [kw][row][output 64]
   const int w0 = kbs * kw >> tw_log2, w1 = kbs * (kw + 1) >> tw_log2, wn = w1 - w0;
@@ -175,7 +179,8 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
   const bool special = MX && __ldg(p.special) != 0u;
 
   // the warp's blocks: output block nb0, nb0 + nb_step, ..., input blocks
-  // [w0, w1) of each.  Scales come with the last block of a group, or of the part.
+  // [w0, w1) of each.  Zeros come with the first block of a group, or of the
+  // part, scales with the last.
   const int bpg = MX ? 1 : p.blocks_per_group;
   const int gr0 = (kb0 + w0) / bpg, in0 = (kb0 + w0) - gr0 * bpg;   // the first block's group, and its place there
   int ld_nb = wn > 0 ? nb0 : p.nblocks, ld_kb = w0, ld_in = in0, ld_slot = 0;
@@ -193,9 +198,9 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
       cp_async<16>(at + lane * 16, ld_code);
       cp_async<16>(at + 512 + lane * 16, ld_code + 32);
       const bool part_end = ld_kb == w1 - 1;
+      if (ZP && (ld_in == 0 || ld_kb == w0) && t < 2) cp_async<4>(at + 1024 + 64 * SB + zp_lane, ld_zp);
       if (MX || ld_in == bpg - 1 || part_end) {
         if (SB > 1 || t < 2) cp_async<SB == 4 ? 8 : 4>(at + 1024 + sc_lane, ld_sc);
-        if (ZP && t < 2) cp_async<4>(at + 1024 + 64 * SB + zp_lane, ld_zp);
         if (!part_end) {
           ld_sc += 64 * SB;
           if (ZP) ld_zp += 64;
@@ -238,30 +243,20 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
                      : __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(p.x) + at + i));
       }
     };
-    // chunk q (8 inputs) of a row, scaled, to its place; the sum of a block's 32 inputs
+    // chunk q (8 inputs) of a row, scaled, to its place
     auto put = [&](int r, int q, bool there, const float* v, float up) {
-      float sum = 0.f;
-      if (there) {
-        uint32_t hi[4], lo[4];
+      if (!there) return;
+      uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float a = v[2 * j] * up, b = v[2 * j + 1] * up;
-          hi[j] = pack_h2(a, b);
-          const __half2 hh = *reinterpret_cast<const __half2*>(&hi[j]);
-          lo[j] = F32 ? pack_h2(a - __low2float(hh), b - __high2float(hh)) : 0u;
-          const __half2 ll = *reinterpret_cast<const __half2*>(&lo[j]);
-          sum += __low2float(hh) + __high2float(hh);
-          if (F32) sum += __low2float(ll) + __high2float(ll);
-        }
-        const int at = ((w0 + (q >> 2)) * R + r) * 4 + (q & 3);
-        xs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (F32) xs[(size_t)kb_max * R * 4 + at] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      for (int j = 0; j < 4; ++j) {
+        const float a = v[2 * j] * up, b = v[2 * j + 1] * up;
+        hi[j] = pack_h2(a, b);
+        const __half2 hh = *reinterpret_cast<const __half2*>(&hi[j]);
+        lo[j] = F32 ? pack_h2(a - __low2float(hh), b - __high2float(hh)) : 0u;
       }
-      if (!MX) {
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-        if (there && t == 0) xsum[(w0 + (q >> 2)) * 8 + r] = sum;
-      }
+      const int at = ((w0 + (q >> 2)) * R + r) * 4 + (q & 3);
+      xs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if (F32) xs[(size_t)kb_max * R * 4 + at] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     };
     // the power of two that takes a row's largest magnitude to [2^14, 2^15); its inverse is kept
     auto scale_row = [&](int r, float most) {
@@ -271,9 +266,10 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
       if (lane == 0 && r < R) unscale[kw * 8 + r] = __uint_as_float((uint32_t)(127 - e) << 23);
       return __uint_as_float((uint32_t)(e + 127) << 23);
     };
-    // A part that fits registers: all its loads in flight at once (7168 x 5120,
-    // 8 rows: 20 us where the loop below reads each row twice, 12 so).  Eight
-    // rows at a time cost the MXFP4 kernel's loop registers and 4 %.
+    // A part that fits registers: its loads of four rows in flight at once (7168 x
+    // 5120, 8 rows: 20 us where the loop below reads each row twice, 12 so).
+    // Eight rows at a time cost MXFP4's loop registers and 4 %, and a single int4
+    // row 0.4 us of code that runs once.
     auto convert_held = [&](auto rows) {
       constexpr int kRows = decltype(rows)::value;
       for (int r0 = team; r0 < R; r0 += kRows * teams) {
@@ -353,7 +349,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
         }
       }
     };
-    if (p.x_vec && wn <= 16) convert_held(std::integral_constant<int, F32 || MX ? 4 : 8>{});
+    if (p.x_vec && wn <= 16) convert_held(std::integral_constant<int, 4>{});
     else if (p.x_vec) convert(std::true_type{}, std::integral_constant<int, 4>{});
     else convert(std::false_type{}, std::integral_constant<int, 1>{});
     if (teams > 1) __syncthreads();
@@ -364,7 +360,9 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
   bool waited = cs == 1;
   for (int nb = nb0; nb < p.nblocks; nb += nb_step, turn ^= 1) {
     float acc[4][4], sum[4][4];
-    float gx[2] = {0.f, 0.f};   // sum of x over the group, rows 2t and 2t + 1
+    uint32_t zlo[4], zhi[4];   // int4: -(1024 + z) of outputs g, -(64 + z) of outputs g + 8, twice each
+#pragma unroll
+    for (int i = 0; i < 4; ++i) zlo[i] = 0xE408E408u, zhi[i] = 0xD480D480u;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -386,9 +384,14 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
         xv[sp] = make_uint4(0u, 0u, 0u, 0u);
         if (g < R) xv[sp] = xs[(size_t)sp * kb_max * R * 4 + (kb * R + g) * 4 + t];
       }
-      if (!MX) {
-        const float2 x2 = *reinterpret_cast<const float2*>(xsum + kb * 8 + 2 * t);
-        gx[0] += x2.x, gx[1] += x2.y;
+      if (ZP && (in == 0 || kb == w0)) {
+        const uint2 zp = *reinterpret_cast<const uint2*>(at + 1024 + 64 * SB + g * 8);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t z = i < 2 ? zp.x : zp.y;
+          zlo[i] = __byte_perm(z, 0xE4u, i & 1 ? 0x4242 : 0x4040);
+          zhi[i] = __byte_perm(z << 4, 0xD4u, i & 1 ? 0x4343 : 0x4141);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -402,21 +405,18 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
                 " cvt.rn.f16x2.e2m1x2 %1, b1;\n cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
                 : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
                 : "r"(w));
-          } else {   // outputs g: q 2^-24; g + 8: q 2^-20
+          } else {   // q - z of outputs g and g + 8 in turn
             const uint32_t v = w >> 8;
-            a[0] = w & 0x000F000Fu;
-            a[1] = w & 0x00F000F0u;
-            a[2] = v & 0x000F000Fu;
-            a[3] = v & 0x00F000F0u;
-            if (F32) {   // q itself: under the exponents of 1024 and, a nibble up, of 64
+            a[0] = under_1024(w, 0x000F000Fu);
+            a[1] = under_1024(w, 0x00F000F0u);
+            a[2] = under_1024(v, 0x000F000Fu);
+            a[3] = under_1024(v, 0x00F000F0u);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                a[j] |= 0x64006400u;
-                const __half2 h = *reinterpret_cast<const __half2*>(&a[j]);
-                const __half2 q = j & 1 ? __hfma2(h, __floats2half2_rn(0.0625f, 0.0625f), __floats2half2_rn(-64.f, -64.f))
-                                        : __hadd2(h, __floats2half2_rn(-1024.f, -1024.f));
-                a[j] = *reinterpret_cast<const uint32_t*>(&q);
-              }
+            for (int j = 0; j < 4; ++j) {
+              const __half2 h = *reinterpret_cast<const __half2*>(&a[j]);
+              const __half2 z = *reinterpret_cast<const __half2*>(j & 1 ? &zhi[i] : &zlo[i]);
+              const __half2 q = j & 1 ? __hfma2(h, __floats2half2_rn(0.0625f, 0.0625f), z) : __hadd2(h, z);
+              a[j] = *reinterpret_cast<const uint32_t*>(&q);
             }
           }
 #pragma unroll
@@ -444,21 +444,13 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s[2 * i + (j >> 1)], sum[i][j], acc[i][j]);
         } else {
-          uint2 zp = make_uint2(0u, 0u);
-          if (ZP) zp = *reinterpret_cast<const uint2*>(at + 1024 + 64 * SB + g * 8);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float s = sc.get(i, e), up = F32 ? 1.f : e ? 1048576.f : 16777216.f;
-              const float z = ZP ? (float)(((i < 2 ? zp.x : zp.y) >> (16 * (i & 1) + 8 * e)) & 15u) : 8.f;
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                acc[i][2 * e + r] = fmaf(s, fmaf(sum[i][2 * e + r], up, -z * gx[r]), acc[i][2 * e + r]);
-                sum[i][2 * e + r] = 0.f;
-              }
+            for (int j = 0; j < 4; ++j) {
+              acc[i][j] = fmaf(sc.get(i, j >> 1), sum[i][j], acc[i][j]);
+              sum[i][j] = 0.f;
             }
-          gx[0] = gx[1] = 0.f;
           in = 0;
         }
       }

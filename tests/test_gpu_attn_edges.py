@@ -234,3 +234,37 @@ def test_attend_values_at_the_ends_of_the_range(m, dtype, d, hq, hk, length, pow
     out = plan.attend(cache, q, i32([length]), i32(table), torch.empty_like(q))
     want, _, ob, _ = R.attend(cache, q, [length], table, [1], page, 1 / math.sqrt(d))
     within(out, want, ob)
+
+
+# ---------------------------------------------------------- 4-bit projections
+
+INT4 = [(128, "bf16", False), (32, "f32", True), (64, "bf16", True), (96, "f32", False), (256, "f32", True)]
+
+
+def near_zero_codes(n, k, group, zeros, span, seed):
+    """Codes that lie within `span` of their zero point."""
+    g = gen(seed)
+    z = torch.randint(span, 16 - span, (n, k // group), device="cuda", generator=g) if zeros else \
+        torch.full((n, k // group), 8, device="cuda")
+    q = z.repeat_interleave(group, 1) + torch.randint(-span, span + 1, (n, k), device="cuda", generator=g)
+    return (q[:, 0::2] | q[:, 1::2] << 4).to(torch.uint8), z.to(torch.uint8) if zeros else None
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("group,scales,zeros", INT4)
+@pytest.mark.parametrize("n,groups", [(64, 1), (70, 9), (1003, 40), (20000, 5)])
+@pytest.mark.parametrize("span", [0, 1])
+def test_project_codes_next_to_the_zero_point(m, dtype, group, scales, zeros, n, groups, span):
+    """Weights that are zero give zero exactly, small ones lose nothing to the
+    zero point's share of the sum; x has a mean."""
+    k = group * groups
+    codes, z = near_zero_codes(n, k, group, zeros, span, 400)
+    s = (torch.rand((n, groups), device="cuda", generator=gen(401)) + 0.1).to(DT[scales])
+    plan = m.Projection(n, k, group=group, scale_dtype=scales, zeros=zeros, dtype=dtype)
+    plan.pack(codes, s, z)
+    full = R.weights(codes, s, z, "int4", group)
+    for rows in (1, 3, 8):
+        x = (normal((rows, k), torch.float32, 402) + 3).to(DT[dtype])
+        y = plan.step(x, torch.empty(rows, n, dtype=DT[dtype], device="cuda"))
+        within(y, *R.project(x, full))
+        assert span or (y == 0).all()
