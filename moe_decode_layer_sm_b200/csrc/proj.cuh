@@ -111,6 +111,11 @@ __device__ __forceinline__ float e8m0_ends(float s) {   // 2^-127 and NaN
   return b == 0u ? __uint_as_float(0x00400000u) : b == 0x7F800000u ? __uint_as_float(0x7FC00000u) : s;
 }
 
+__device__ __forceinline__ float finite_max(float m, float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? fmaxf(m, a) : m;
+}
+
 // (w & mask) | 0x64006400, in one instruction (as two: 7168 x 5120 int4, 1 row, 9.4 us; 7.9 so)
 __device__ __forceinline__ uint32_t under_1024(uint32_t w, uint32_t mask) {
   uint32_t r;
@@ -252,17 +257,22 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
         const float a = v[2 * j] * up, b = v[2 * j + 1] * up;
         hi[j] = pack_h2(a, b);
         const __half2 hh = *reinterpret_cast<const __half2*>(&hi[j]);
-        lo[j] = F32 ? pack_h2(a - __low2float(hh), b - __high2float(hh)) : 0u;
+        // (an infinity's second term, inf - inf, may be any number)
+        lo[j] = F32 ? pack_h2(fmaxf(a - __low2float(hh), -64.f), fmaxf(b - __high2float(hh), -64.f)) : 0u;
       }
       const int at = ((w0 + (q >> 2)) * R + r) * 4 + (q & 3);
       xs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       if (F32) xs[(size_t)kb_max * R * 4 + at] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     };
-    // the power of two that takes a row's largest magnitude to [2^14, 2^15); its inverse is kept
-    auto scale_row = [&](int r, float most) {
-      most = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(most)));
+    // The power of two that takes a row's largest magnitude to [2^14, 2^15); its
+    // inverse is kept.  Beside infinities the largest finite one counts, which
+    // `again` finds: the others must not become infinite too.
+    auto scale_row = [&](int r, float most, auto again) {
+      auto of_warp = [](float v) { return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v))); };
+      most = of_warp(most);
+      if (!(most <= 3.402823466e38f)) most = of_warp(again());
       int e = 14 - ((int)(__float_as_uint(most) >> 23) - 127);
-      e = most > 0.f && most <= 3.402823466e38f ? min(e, 100) : 0;
+      e = most > 0.f ? min(e, 100) : 0;
       if (lane == 0 && r < R) unscale[kw * 8 + r] = __uint_as_float((uint32_t)(127 - e) << 23);
       return __uint_as_float((uint32_t)(e + 127) << 23);
     };
@@ -309,7 +319,14 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
 #pragma unroll
             for (int j = 0; j < 8; ++j) most = fmaxf(most, fabsf(v[k][j]));
           }
-          const float up = scale_row(r, most);
+          const float up = scale_row(r, most, [&] {
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) m = finite_max(m, v[k][j]);
+            return m;
+          });
 #pragma unroll
           for (int k = 0; k < 2; ++k) put(r, lane + 32 * k, lane + 32 * k < wn * 4, v[k], up);
         }
@@ -334,7 +351,17 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
             }
           }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) amax[i] = scale_row(r0 + i * teams, amax[i]);
+        for (int i = 0; i < kRows; ++i)
+          amax[i] = scale_row(r0 + i * teams, amax[i], [&] {
+            float m = 0.f;
+            for (int q = lane; q < wn * 4; q += 32) {
+              float v[8];
+              get8(vec, r0 + i * teams, q, v);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) m = finite_max(m, v[j]);
+            }
+            return m;
+          });
         for (int q0 = 0; q0 < wn * 4; q0 += 32) {
           const int q = q0 + lane;
 #pragma unroll

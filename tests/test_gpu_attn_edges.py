@@ -268,3 +268,46 @@ def test_project_codes_next_to_the_zero_point(m, dtype, group, scales, zeros, n,
         y = plan.step(x, torch.empty(rows, n, dtype=DT[dtype], device="cuda"))
         within(y, *R.project(x, full))
         assert span or (y == 0).all()
+
+
+KINDS = [("int4", 64, "f32", True), ("int4", 128, "bf16", False), ("mxfp4", 32, "bf16", False)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,group,scales,zeros", KINDS)
+@pytest.mark.parametrize("n,k,shift", [(130, 512, 0), (130, 512, 1), (7, 1280, 0), (9500, 6400, 0)])
+def test_project_infinities(m, dtype, fmt, group, scales, zeros, n, k, shift):
+    """x of +-infinity gives what the sum of products gives: infinities of the
+    weights' signs, NaN where a weight is zero or two of them meet; finite
+    numbers beside them that no fp16 holds change nothing."""
+    w = make_weights(n, k, fmt, group, scales, zeros, 410)
+    plan = m.Projection(n, k, fmt=fmt, group=group, scale_dtype=scales, zeros=zeros, dtype=dtype)
+    plan.pack(*w)
+    full = R.weights(*w, fmt, group)
+    x = normal((6, k + 8), DT[dtype], 411)[:, shift:shift + k]
+    x[0, 5] = math.inf
+    x[1, k - 1] = -math.inf
+    x[2, 7], x[2, k - 9] = math.inf, math.inf
+    x[3, 100], x[3, ::3] = math.inf, -1e20
+    x[4, 6], x[4, 300] = math.inf, math.nan
+    y = plan.step(x, torch.empty(6, n, dtype=DT[dtype], device="cuda"))
+    prod = torch.stack([(x[r].double() * full).sum(1) for r in range(6)])   # (a product for each weight, then their sum)
+    got = y.double()
+    assert torch.equal(torch.isnan(got), torch.isnan(prod))
+    assert torch.equal(torch.isposinf(got), torch.isposinf(prod)) and torch.equal(torch.isneginf(got), torch.isneginf(prod))
+    assert torch.isposinf(prod).any() and torch.isneginf(prod).any() and torch.isfinite(prod[5]).all()
+    within(y[5:], *R.project(x[5:], full))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt,group,scales,zeros", KINDS)
+def test_project_long_parts(m, dtype, fmt, group, scales, zeros):
+    """More than 16 blocks of inputs a warp (bf16): x is read twice, not held."""
+    n, k = 9500, 6400
+    w = make_weights(n, k, fmt, group, scales, zeros, 415)
+    plan = m.Projection(n, k, fmt=fmt, group=group, scale_dtype=scales, zeros=zeros, dtype=dtype)
+    plan.pack(*w)
+    for rows in (1, 8):
+        x = normal((rows, k), DT[dtype], 416)
+        y = plan.step(x, torch.empty(rows, n, dtype=DT[dtype], device="cuda"))
+        within(y, *R.project(x, R.weights(*w, fmt, group)))
