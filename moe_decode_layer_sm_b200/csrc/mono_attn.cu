@@ -697,7 +697,7 @@ extern "C" int mono_proj_plan(const mono_proj_config* c, mono_proj_plan_t** out)
     cudaError_t e = dalloc(&p->codes, (size_t)p->nblocks * kblocks * 1024, &p->packed);
     if (e == cudaSuccess) e = dalloc(&p->scales, n64 * sb, &p->packed);
     if (e == cudaSuccess && c->zeros) e = dalloc(&p->zeros, n64, &p->packed);
-    if (e == cudaSuccess && mx) e = dalloc(&p->special, 4, &p->packed);
+    if (e == cudaSuccess) e = dalloc(&p->special, 4, &p->packed);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(proj_for(f32, p->sc, c->zeros != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)kSmemMax);
@@ -726,22 +726,20 @@ extern "C" int mono_proj_pack(mono_proj_plan_t* p, const void* codes, const void
     auto grid = [&](long long n) { return (unsigned)std::min<long long>((n + 255) / 256, 148LL * 64); };
     pack_proj_codes_kernel<<<grid(words), 256, 0, st>>>((const uint8_t*)codes, (uint32_t*)p->codes, p->cfg.n_out,
                                                          p->cfg.n_in, words, p->cfg.format == MONO_MXFP4);
-    if (p->special) {
-      const cudaError_t e = cudaMemsetAsync(p->special, 0, 4, st);
-      if (e != cudaSuccess) return cuda_fail(e, "proj_pack");
-    }
+    const cudaError_t cleared = cudaMemsetAsync(p->special, 0, 4, st);
+    if (cleared != cudaSuccess) return cuda_fail(cleared, "proj_pack");
     if (p->sc == kScaleBf16)
       pack_proj_groups_kernel<<<grid(n64), 256, 0, st>>>((const uint16_t*)scales, (uint16_t*)p->scales, p->cfg.n_out,
-                                                          p->groups, n64, 0, nullptr);
+                                                          p->groups, n64, 0, p->special, 0x7FFFu, (127u + 64u) << 7);
     else if (p->sc == kScaleF32)
       pack_proj_groups_kernel<<<grid(n64), 256, 0, st>>>((const uint32_t*)scales, (uint32_t*)p->scales, p->cfg.n_out,
-                                                          p->groups, n64, 0, nullptr);
+                                                          p->groups, n64, 0, p->special, 0x7FFFFFFFu, (127u + 64u) << 23);
     else
       pack_proj_groups_kernel<<<grid(n64), 256, 0, st>>>((const uint8_t*)scales, p->scales, p->cfg.n_out, p->groups,
-                                                          n64, 0, p->special);
+                                                          n64, 0, p->special, 0xFFu, 127u + 64u);
     if (zeros)
       pack_proj_groups_kernel<<<grid(n64), 256, 0, st>>>((const uint8_t*)zeros, p->zeros, p->cfg.n_out, p->groups, n64,
-                                                          15, nullptr);
+                                                          15, nullptr, 0u, 0u);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "proj_pack");
     p->is_packed = true;

@@ -10,6 +10,9 @@ namespace mono {
 
 enum { kScaleBf16 = 0, kScaleF32 = 1, kScaleE8m0 = 2 };
 
+// MXFP4: a scale byte is 0 or 255; a scale is 2^64 or more (or no number)
+enum { kEnds = 1, kLarge = 2 };
+
 struct ProjParams {
   const uint8_t* codes;    // packed, see pack_proj_codes_kernel
   const uint8_t* scales;   // packed
@@ -17,7 +20,7 @@ struct ProjParams {
   const void* x;
   void* y;
   long long x_row, y_row;
-  const unsigned int* special;   // MXFP4: nonzero where a scale byte is 0 or 255
+  const unsigned int* special;   // kEnds, kLarge: what scales there are
   int rows, n_out, kblocks, blocks_per_group, groups, nblocks, x_vec;
   int teams_log2;     // output blocks that a CTA works on at once, each with kProjWarps / teams warps
   int cluster_log2;   // CTAs that share an output block's inputs
@@ -61,10 +64,12 @@ __global__ void pack_proj_codes_kernel(const uint8_t* __restrict__ src, uint32_t
 }
 
 // Packed scales and zeros: [nblock][group][g 8][tile 4][output g, g + 8]: a
-// lane's eight values of a group lie together.
+// lane's eight values of a group lie together.  special: kEnds and kLarge among
+// the scales, by `magnitude` (all bits but a sign) and the bits of 2^64, `large`.
 template <typename T>
 __global__ void pack_proj_groups_kernel(const T* __restrict__ src, T* __restrict__ dst, int n_out, int groups,
-                                        long long total, int mask, unsigned int* special) {
+                                        long long total, int mask, unsigned int* special, unsigned int magnitude,
+                                        unsigned int large) {
   for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < total;
        i += (long long)gridDim.x * blockDim.x) {
     const int e = i & 1, tile = (i >> 1) & 3, g = (i >> 3) & 7;
@@ -74,7 +79,11 @@ __global__ void pack_proj_groups_kernel(const T* __restrict__ src, T* __restrict
     T v = T(0);
     if (n < n_out) v = src[n * groups + gr];
     if (mask) v = T((int)v & mask);
-    if (special && n < n_out && (v == T(0) || v == T(255))) atomicOr(special, 1u);
+    if (special && n < n_out) {
+      const unsigned int found = (sizeof(T) == 1 && (v == T(0) || v == T(255)) ? kEnds : 0u) |
+                                 (((unsigned int)v & magnitude) >= large ? kLarge : 0u);
+      if (found) atomicOr(special, found);
+    }
     dst[i] = v;
   }
 }
@@ -181,7 +190,8 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
   const int nclusters = gridDim.x >> p.cluster_log2, cl = blockIdx.x >> p.cluster_log2;
   const int nb0 = (cl << p.teams_log2) + team, nb_step = nclusters << p.teams_log2;
   if (cs > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // waited for before the first push
-  const bool special = MX && __ldg(p.special) != 0u;
+  const unsigned int special = __ldg(p.special);
+  const bool large = (special & kLarge) != 0u;
 
   // the warp's blocks: output block nb0, nb0 + nb_step, ..., input blocks
   // [w0, w1) of each.  Zeros come with the first block of a group, or of the
@@ -458,11 +468,25 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
       if (MX || last || kb == w1 - 1) {
         ScaleRegs<SC> sc;
         sc.load(at + 1024 + g * 8 * SB);
-        if (MX) {
+        // The sums carry the rows' powers of two until the end.  With scales of
+        // 2^64 or more in the plan they could pass fp32's end so; there a row's is
+        // taken off first, after the scale where that is below 1.
+        if (large) {
+          const float un[2] = {unscale[kw * 8 + 2 * t], unscale[kw * 8 + 2 * t + 1]};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float s = MX ? e8m0_ends(sc.get(i, j >> 1)) : sc.get(i, j >> 1), u = un[j & 1];
+              acc[i][j] = fabsf(s) >= 1.f ? fmaf(s, sum[i][j] * u, acc[i][j]) : fmaf(s * sum[i][j], u, acc[i][j]);
+              sum[i][j] = 0.f;
+            }
+          in = 0;
+        } else if (MX) {
           float s[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) s[i] = sc.get(i >> 1, i & 1);
-          if (special) {
+          if (special & kEnds) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i] = e8m0_ends(s[i]);
           }
@@ -488,7 +512,7 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
 #pragma unroll
     for (int r = 0; r < 2; ++r)
       if (2 * t + r < R) {
-        const float un = unscale[kw * 8 + 2 * t + r];
+        const float un = large ? 1.f : unscale[kw * 8 + 2 * t + r];
         float* to = red + (kw * R + 2 * t + r) * kProjRedRow + g;
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -311,3 +311,41 @@ def test_project_long_parts(m, dtype, fmt, group, scales, zeros):
         x = normal((rows, k), DT[dtype], 416)
         y = plan.step(x, torch.empty(rows, n, dtype=DT[dtype], device="cuda"))
         within(y, *R.project(x, R.weights(*w, fmt, group)))
+
+
+def check_project(m, dtype, fmt, codes, scales, zeros, xs, group=32, scale_dtype="f32", more=0.0):
+    n, k = codes.shape[0], codes.shape[1] * 2
+    plan = m.Projection(n, k, fmt=fmt, group=group, scale_dtype=scale_dtype, zeros=zeros is not None, dtype=dtype)
+    plan.pack(codes, scales, zeros)
+    full = R.weights(codes, scales, zeros, fmt, group)
+    for x in xs:
+        y = plan.step(x, torch.empty(x.shape[0], n, dtype=x.dtype, device="cuda"))
+        want, bound = R.project(x, full)
+        assert torch.isfinite(want.to(x.dtype)).all()
+        within(y, want, bound + more)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,k", [(64, 64), (130, 4096), (9500, 256)])
+def test_project_large_scales(m, dtype, n, k):
+    """Scales up to 2^113 with rows whose results are finite, and scales of both
+    ends in one plan.  Results among the subnormals: half their spacing for each
+    sum, and for the output's own rounding."""
+    g = gen(420)
+    more = (k / 32 + 20) * 2.0 ** -149 + (2.0 ** -134 if dtype == "bf16" else 0.0)
+    codes, _, _ = make_weights(n, k, "mxfp4", 32, None, False, 421)
+    x = normal((4, k), DT[dtype], 422)
+    mixed = x * torch.tensor([1e-18, 1e-8, 2.0 ** -20, 2.0 ** -12], device="cuda")[:, None].to(x.dtype)
+    for lo, hi in ((236, 237), (230, 240), (1, 240), (238, 239)):
+        s = torch.randint(lo, hi, (n, k // 32), dtype=torch.uint8, device="cuda", generator=g)
+        check_project(m, dtype, "mxfp4", codes, s, None, [mixed], more=more)
+    s = torch.full((n, k // 32), 5, dtype=torch.uint8, device="cuda")
+    s[0] = 230   # one output's are large, the others' results among the subnormals
+    check_project(m, dtype, "mxfp4", codes, s, None, [mixed, x * 1e-3], more=more)
+    for sd in ("f32", "bf16"):
+        s = ((torch.rand((n, k // 32), device="cuda", generator=g) + 0.5) * 2.0 ** 108)
+        s[:, ::2] *= 2.0 ** -200
+        s = (s * torch.where(torch.rand((n, k // 32), device="cuda", generator=g) < 0.5, -1.0, 1.0)).to(DT[sd])
+        z = torch.randint(0, 16, (n, k // 32), dtype=torch.uint8, device="cuda", generator=g)
+        for zeros in (None, z):
+            check_project(m, dtype, "int4", codes, s, zeros, [mixed], scale_dtype=sd, more=more)
