@@ -274,15 +274,15 @@ __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_cons
       xs[at] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       if (F32) xs[(size_t)kb_max * R * 4 + at] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     };
-    // The power of two that takes a row's largest magnitude to [2^14, 2^15); its
-    // inverse is kept.  Beside infinities the largest finite one counts, which
-    // `again` finds: the others must not become infinite too.
+    // The power of two that takes a row's largest magnitude to [2^14, 2^15), 2^126
+    // at most; its inverse is kept.  Beside infinities the largest finite one
+    // counts, which `again` finds: the others must not become infinite too.
     auto scale_row = [&](int r, float most, auto again) {
       auto of_warp = [](float v) { return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v))); };
       most = of_warp(most);
       if (!(most <= 3.402823466e38f)) most = of_warp(again());
       int e = 14 - ((int)(__float_as_uint(most) >> 23) - 127);
-      e = most > 0.f ? min(e, 100) : 0;
+      e = most > 0.f ? min(e, 126) : 0;   // 2^e and 2^-e are both normal
       if (lane == 0 && r < R) unscale[kw * 8 + r] = __uint_as_float((uint32_t)(127 - e) << 23);
       return __uint_as_float((uint32_t)(e + 127) << 23);
     };

@@ -349,3 +349,18 @@ def test_project_large_scales(m, dtype, n, k):
         z = torch.randint(0, 16, (n, k // 32), dtype=torch.uint8, device="cuda", generator=g)
         for zeros in (None, z):
             check_project(m, dtype, "int4", codes, s, zeros, [mixed], scale_dtype=sd, more=more)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("power", [-100, -112, -120, -126, -132])
+def test_project_rows_of_tiny_numbers(m, dtype, power):
+    """Rows whose largest number is near or among fp32's subnormals.  x enters as
+    fp16 after a factor of at most 2^126: halves of fp16's smallest step, 2^-25,
+    are 2^-151 of x, for each weight; with scales of 2^100 the results are usual."""
+    n, k = 130, 512
+    x = (normal((4, k), torch.float64, 430) * 2.0 ** power).to(DT[dtype])
+    for fmt in ("int4", "mxfp4"):
+        codes, s, _ = make_weights(n, k, fmt, 32, "f32", False, 431)
+        s = torch.full_like(s, 227 if fmt == "mxfp4" else 2.0 ** 100)
+        full = R.weights(codes, s, None, fmt, 32)
+        check_project(m, dtype, fmt, codes, s, None, [x], more=2.0 ** -151 * full.abs().sum(1))
