@@ -237,10 +237,10 @@ int mono_proj_pack(mono_proj_plan_t* plan, const void* codes, const void* scales
  * and y_row elements apart.  Products are exact and sums fp32; y is rounded
  * once.  x enters with 11 bits below each row's largest finite magnitude that one
  * warp reads down to 2^-29 of it (bf16 is exact there), MONO_F32 with 22, and
- * below 2^-112 in steps of 2^-150.  An
- * infinity in x gives what the sum of products has: infinities of the weights'
- * signs, NaN where a weight is zero or two of them meet.  y may not overlap x.
- * Uses no scratch: calls on one plan may overlap. */
+ * below 2^-112 in steps of 2^-150.  An infinity in x gives what the sum of
+ * products has: infinities of the weights' signs, NaN where a weight is zero or
+ * two of them meet.  y may not overlap x.  Uses no scratch: calls on one plan
+ * may overlap. */
 int mono_proj_step(mono_proj_plan_t* plan, int rows, const void* x, int64_t x_row, void* y, int64_t y_row,
                    void* stream);
 

@@ -36,12 +36,16 @@ bool entries(const at::Tensor* t, int64_t device, int64_t n, int64_t m) {
          t->size(0) == n && (m < 0 || t->size(1) == m);
 }
 
+// Memory that is written.  Taking its address gives a lazily cloned tensor
+// storage of its own, so it comes before that of tensors which may share it.
+void* written(const at::Tensor* t) { return t->mutable_data_ptr(); }
+
 // [seqs][width][heads][head_dim] with a contiguous last dimension
-bool rows(const at::Tensor* t, int64_t device, int64_t type, int64_t heads, int64_t head_dim, mono_rows* r) {
+bool rows(const at::Tensor* t, int64_t device, int64_t type, int64_t heads, int64_t head_dim, bool out, mono_rows* r) {
   if (!on(t, device) || t->scalar_type() != type_of(type) || t->dim() != 4 || t->size(2) != heads ||
       t->size(3) != head_dim || t->stride(3) != 1)
     return false;
-  *r = mono_rows{const_cast<void*>(t->const_data_ptr()), t->stride(0), t->stride(1), t->stride(2)};
+  *r = mono_rows{out ? written(t) : const_cast<void*>(t->const_data_ptr()), t->stride(0), t->stride(1), t->stride(2)};
   return true;
 }
 
@@ -81,10 +85,11 @@ PyObject* call_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int transpose = PyObject_IsTrue(a[4]) == 1;
     void* stream = stream_of(a[5], dev);
     const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    void* to = written(out);
     return enter([&] {
       return mono_rope_apply(rope, (int)tokens, (int)heads, (int)x->size(2), type == at::kFloat ? MONO_F32 : MONO_BF16,
                              x->const_data_ptr(), x->stride(0), x->stride(1), static_cast<const int*>(pos->const_data_ptr()),
-                             const_cast<void*>(out->const_data_ptr()), out->stride(0), out->stride(1), transpose, stream);
+                             to, out->stride(0), out->stride(1), transpose, stream);
     });
   });
 }
@@ -94,11 +99,11 @@ PyObject* call_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 struct Call {
   mono_rows x, y;
   mono_seqs seqs;
-  bool take(PyObject* const* a) {
+  bool take(PyObject* const* a, bool y_out) {
     const int64_t heads = number(a[2]), head_dim = number(a[3]), type = number(a[4]), dev = number(a[5]);
     const at::Tensor *tx = tensor(a[7]), *ty = tensor(a[8]), *lens = tensor(a[9]), *table = tensor(a[10]);
     const at::Tensor* n_new = a[11] == Py_None ? nullptr : tensor(a[11]);
-    if (!rows(tx, dev, type, heads, head_dim, &x) || !rows(ty, dev, type, heads, head_dim, &y)) return false;
+    if (!rows(ty, dev, type, heads, head_dim, y_out, &y) || !rows(tx, dev, type, heads, head_dim, false, &x)) return false;
     const int64_t n = tx->size(0), width = tx->size(1);
     if (ty->size(0) != n || ty->size(1) != width || n > INT_MAX || width > INT_MAX || !entries(lens, dev, n, -1) ||
         !entries(table, dev, n, number(a[6])) || (a[11] != Py_None && !entries(n_new, dev, n, -1)))
@@ -114,7 +119,7 @@ struct Call {
 PyObject* call_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> long {
     Call c;
-    if (n != 14 || !c.take(a)) return kNotTaken;
+    if (n != 14 || !c.take(a, false)) return kNotTaken;
     auto* plan = static_cast<mono_attn_plan_t*>(address(a[0]));
     const auto* cache = static_cast<const mono_kv_cache*>(address(a[1]));
     const auto* rope = static_cast<const mono_rope*>(address(a[12]));
@@ -127,14 +132,14 @@ PyObject* call_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* call_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> long {
     Call c;
-    if (n != 14 || !c.take(a)) return kNotTaken;
+    if (n != 14 || !c.take(a, true)) return kNotTaken;
     float* lse = nullptr;
     if (a[12] != Py_None) {
       const at::Tensor* t = tensor(a[12]);
       if (!on(t, number(a[5])) || t->scalar_type() != at::kFloat || t->dim() != 3 || t->size(0) != c.seqs.seqs ||
           t->size(1) != c.seqs.width || t->size(2) != number(a[2]) || !t->is_contiguous())
         return kNotTaken;
-      lse = static_cast<float*>(const_cast<void*>(t->const_data_ptr()));
+      lse = static_cast<float*>(written(t));
     }
     auto* plan = static_cast<mono_attn_plan_t*>(address(a[0]));
     const auto* cache = static_cast<const mono_kv_cache*>(address(a[1]));
@@ -156,9 +161,9 @@ PyObject* call_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return kNotTaken;
     auto* plan = static_cast<mono_proj_plan_t*>(address(a[0]));
     void* stream = stream_of(a[7], dev);
+    void* to = written(y);
     return enter([&] {
-      return mono_proj_step(plan, (int)x->size(0), x->const_data_ptr(), x->stride(0), const_cast<void*>(y->const_data_ptr()),
-                            y->stride(0), stream);
+      return mono_proj_step(plan, (int)x->size(0), x->const_data_ptr(), x->stride(0), to, y->stride(0), stream);
     });
   });
 }

@@ -364,3 +364,33 @@ def test_project_rows_of_tiny_numbers(m, dtype, power):
         s = torch.full_like(s, 227 if fmt == "mxfp4" else 2.0 ** 100)
         full = R.weights(codes, s, None, fmt, 32)
         check_project(m, dtype, fmt, codes, s, None, [x], more=2.0 ** -151 * full.abs().sum(1))
+
+
+# ------------------------------------------------- outputs that share storage
+
+def test_outputs_that_share_storage_lazily(m):
+    """A lazily cloned output is given storage of its own before it is written."""
+    r, pos = m.Rope(64), i32([3, 9])
+    x = normal((2, 2, 64), torch.float32, 440)
+    want = m.rope(x, pos, r, out=torch.empty_like(x))
+    base = torch.full_like(x, 3.0)
+    out = torch._lazy_clone(base)
+    m.rope(x, pos, r, out=out)
+    assert (base == 3.0).all() and torch.equal(out, want)
+    again = torch._lazy_clone(x)   # in place
+    before = x.clone()
+    m.rope(again, pos, r)
+    assert torch.equal(x, before) and torch.equal(again, want)
+    plan = m.Projection(64, 64, group=32)
+    plan.pack(*make_weights(64, 64, "int4", 32, "bf16", False, 441))
+    xb = normal((2, 64), torch.bfloat16, 442)
+    base = torch.full((2, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    y = plan.step(xb, torch._lazy_clone(base))
+    assert (base == 3.0).all() and torch.equal(y, plan.step(xb, torch.empty_like(base)))
+    cache = make_cache(m, 2, 2, 16, 64, 443)
+    attn = m.AttnPlan(4, 2, 64, 16, 2, 1, 2)
+    q = normal((1, 1, 4, 64), torch.bfloat16, 444)
+    base, lbase = torch.full_like(q, 3.0), torch.full((1, 1, 4), 3.0, device="cuda")
+    out, lse = torch._lazy_clone(base), torch._lazy_clone(lbase)
+    attn.attend(cache, q, i32([20]), i32([[1, 0]]), out, lse=lse)
+    assert (base == 3.0).all() and (lbase == 3.0).all() and not (out == 3.0).all() and not (lse == 3.0).any()
