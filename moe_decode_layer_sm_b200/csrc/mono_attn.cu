@@ -591,7 +591,7 @@ extern "C" int mono_attn_query_error(mono_attn_plan_t* p, mono_attn_status* st) 
 }
 
 extern "C" int mono_attn_get_info(const mono_attn_plan_t* p, mono_attn_info* info) {
-  if (!p || !info) return MONO_ERR_INVALID_ARG;
+  if (!p || !info) return guarded([] { return fail(MONO_ERR_INVALID_ARG, "attn_get_info: NULL argument"); });
   info->grid = std::max(std::max(p->grid[0][0], p->grid[0][1]), std::max(p->grid[1][0], p->grid[1][1]));
   info->scratch_bytes = p->scratch;
   return MONO_OK;
@@ -808,7 +808,7 @@ extern "C" int mono_proj_step(mono_proj_plan_t* p, int rows, const void* x, int6
 }
 
 extern "C" int mono_proj_get_info(const mono_proj_plan_t* p, mono_proj_info* info) {
-  if (!p || !info) return MONO_ERR_INVALID_ARG;
+  if (!p || !info) return guarded([] { return fail(MONO_ERR_INVALID_ARG, "proj_get_info: NULL argument"); });
   info->cluster = p->cluster;
   info->packed_bytes = p->packed;
   return MONO_OK;

@@ -296,3 +296,11 @@ def test_more_new_tokens_than_rows_have_no_work(idx):
         for lead in (0, 3):
             assert idx.tiles(length, 9, 8, 1024, 0, 32, lead) == 0
             assert idx.tiles(length, 8, 8, 1024, 0, 32, lead) > lead
+
+
+def test_get_info_says_what_is_wrong(attn):
+    """Not the reason of the call before it."""
+    L = attn._lib()
+    assert L.mono_rope_init(None, None) == -1
+    for f, frag in ((L.mono_attn_get_info, "attn_get_info"), (L.mono_proj_get_info, "proj_get_info")):
+        assert f(None, None) == -1 and frag in L.mono_attn_last_error().decode()
