@@ -91,7 +91,11 @@ def _lib():
             getattr(L, f).restype = None
         L.mono_attn_last_error.argtypes = []
         L.mono_attn_last_error.restype = ctypes.c_char_p
-        from . import _call as compiled
+        try:
+            from . import _call as compiled
+        except ImportError as e:
+            raise RuntimeError("_call.so is missing: build it with __graft_entry__.build() (g++, Python's headers, "
+                               "torch)") from e
         _call, _ready = compiled, L
     return _ready
 

@@ -7,9 +7,12 @@ has a later modification time than its sources is not trusted.  Each
 translation unit keeps an object with a stamp of its own.
 
 _call.so, the compiled part of the attention half's binding, is built beside it
-with g++ against the installed torch and has its own stamp."""
+with g++ against the installed torch and has its own stamp.  Where torch or
+Python's headers are missing the library is built alone: the C ABI and the FFN
+binding need no more, and attn.py then says what it misses."""
 
 import hashlib
+import importlib.util
 import os
 import subprocess
 import sys
@@ -104,7 +107,14 @@ def call_hash():
     return h.hexdigest()
 
 
+def can_build_call():
+    return importlib.util.find_spec("torch") is not None and \
+        os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
 def build_call(force=False):
+    if not can_build_call():
+        return None
     stamp = CALL + ".sha256"
     if not force and os.path.exists(CALL) and os.path.exists(stamp):
         with open(stamp) as f:
