@@ -548,14 +548,15 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
         uint32_t pf[kSubs][NT][kSplit][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          const float off0 = mx[n][0] == -INFINITY ? 0.f : mx[n][0] - kPBias;
-          const float off1 = mx[n][1] == -INFINITY ? 0.f : mx[n][1] - kPBias;
+          // the difference first: it is 0 for the largest logit, whose probability is 1
+          const float off0 = mx[n][0] == -INFINITY ? 0.f : mx[n][0];
+          const float off1 = mx[n][1] == -INFINITY ? 0.f : mx[n][1];
 #pragma unroll
           for (int b = 0; b < kSubs; ++b) {
             float e[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              e[j] = exp2_approx(c[b][n][j] - (j & 1 ? off1 : off0));
+              e[j] = exp2_approx(c[b][n][j] - (j & 1 ? off1 : off0) + kPBias);
               l[n][j & 1] += e[j];
             }
             // a scale that is no finite number: only what sees the page's tokens meets it

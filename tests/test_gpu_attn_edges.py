@@ -394,3 +394,19 @@ def test_outputs_that_share_storage_lazily(m):
     out, lse = torch._lazy_clone(base), torch._lazy_clone(lbase)
     attn.attend(cache, q, i32([20]), i32([[1, 0]]), out, lse=lse)
     assert (base == 3.0).all() and (lbase == 3.0).all() and not (out == 3.0).all() and not (lse == 3.0).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,hq,hk", [(64, 8, 8), (64, 64, 4), (128, 40, 8), (128, 24, 2), (256, 16, 8)])
+def test_attend_one_token_is_exact(m, dtype, d, hq, hk):
+    """Its probability is 1 whatever its logit: the output is the value, the
+    product of its code and scale in fp32, also where that is a tie between two
+    bf16 numbers (scales of 8 bits make many)."""
+    for seed in range(6):
+        cache = make_cache(m, 4, hk, 16, d, 450 + seed)
+        cache.v_scale.copy_(cache.v_scale.bfloat16())
+        q = normal((2, 1, hq, d), DT[dtype], 460 + seed) * 2.0 ** (seed - 2)
+        plan = m.AttnPlan(hq, hk, d, 16, 4, 2, 2, dtype=dtype)
+        out = plan.attend(cache, q, i32([1, 1]), i32([[0, 0], [3, 0]]), torch.empty_like(q))
+        v = cache.v[[0, 3], :, 0].float() * cache.v_scale[[0, 3]][:, :, None]
+        assert torch.equal(out[:, 0], v.repeat_interleave(hq // hk, 1).to(DT[dtype]))
