@@ -582,7 +582,11 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
 #pragma unroll
         for (int b = 0; b < kSubs; ++b) {
           if (!(fabsf(vsc[b]) <= 3.402823466e38f)) vsc[b] = 1.f;
-          const float vs = F32 ? vsc[b] : vsc[b] * kPUnit;   // (inexact below 2^-111, where bf16 rows keep at least 8 bits)
+          // A scale times 2^-15 is inexact below 2^-111.  bf16 rows keep at least 8 bits
+          // of it; fp32 rows take the 2^-15 off the products there (for every scale:
+          // registers spilled, 3 %; the branch in bf16 rows 2 %).
+          const bool low = F32 && fabsf(vsc[b]) < 0x1p-100f;
+          const float vs = low ? vsc[b] : vsc[b] * kPUnit;
           uint32_t vw[4][S::kValWords];   // tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -668,8 +672,9 @@ __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) /
               float o[4];
               mma_f16_first(o, a, pf[b][n][0][0], pf[b][n][0][1]);
               if (F32) mma_f16(o, a, pf[b][n][kSplit - 1][0], pf[b][n][kSplit - 1][1]);
+              if (low) o[0] *= kPUnit, o[1] *= kPUnit, o[2] *= kPUnit, o[3] *= kPUnit;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) O[w][n][j] = fmaf(F32 ? o[j] * kPUnit : o[j], vs, O[w][n][j]);
+              for (int j = 0; j < 4; ++j) O[w][n][j] = fmaf(o[j], vs, O[w][n][j]);
             }
           }
         }

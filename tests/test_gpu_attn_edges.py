@@ -410,3 +410,26 @@ def test_attend_one_token_is_exact(m, dtype, d, hq, hk):
         out = plan.attend(cache, q, i32([1, 1]), i32([[0, 0], [3, 0]]), torch.empty_like(q))
         v = cache.v[[0, 3], :, 0].float() * cache.v_scale[[0, 3]][:, :, None]
         assert torch.equal(out[:, 0], v.repeat_interleave(hq // hk, 1).to(DT[dtype]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 24, 2), (256, 4, 2)])
+def test_attend_smallest_scales(m, dtype, d, hq, hk):
+    """Page scales from 2^-126 up beside usual ones that other rows see.  Beyond
+    the usual bound: half of fp32's smallest step for each group of 16 tokens and
+    the joins, the output's own smallest half step, and for bf16 rows a scale in
+    steps of 2^-134, half of one times codes up to 448."""
+    page, length = 64, 700
+    pages = -(-length // page)
+    cache = make_cache(m, pages + 1, hk, page, d, 470)
+    cache.v_scale[:pages] = cache.v_scale[:pages] * 2.0 ** -119
+    cache.v_scale[2] = 2.0 ** -126
+    q = normal((2, 1, hq, d), DT[dtype], 471)
+    table = [list(range(pages)), [pages] + [-1] * (pages - 1)]
+    plan = m.AttnPlan(hq, hk, d, page, pages + 1, 2, pages, dtype=dtype)
+    out = plan.attend(cache, q, i32([length, 50]), i32(table), torch.empty_like(q))
+    want, _, ob, _ = R.attend(cache, q, [length, 50], table, [1, 1], page, 1 / math.sqrt(d))
+    more = (length / 16 + 40) * 2.0 ** -150
+    if dtype == "bf16":
+        more += 2.0 ** -134 + 448 * 2.0 ** -135
+    within(out, want, ob + more)
