@@ -185,15 +185,17 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 // input is read once, and the next heads' are on their way meanwhile.
 //
 // The rotation is done in binary64 and a code near a border is found from it
-// again, so codes and scales are those of the exact rotated values: a key's
-// code does not depend on which call, or which neighbours, it was written
-// with.  Two sines and cosines a pair and page, shared by its heads, give all
+// again, so codes and scales are those of the exact rotated values, rounded
+// once.  (A page's scale goes by all the tokens that a call writes to it, and
+// older codes are rounded again where it grows: a page filled token by token
+// may hold other codes than one written at once.)  Two sines and cosines a pair and page, shared by its heads, give all
 // the others by turning; a thread holds both halves of its pairs, so a value
 // costs one conversion each way and four binary64 operations.
 //
-// Measured: 10486 tokens of 4 prompts, 8 heads of 128, bf16, rotated 42 us, not
-// rotated 32 (64 MB: 10 us of memory); bound by instructions, of which a head's
-// and a CTA's own are more than the values'.  One token of 8 sequences 3.6 us.
+// Measured: 10486 tokens of 4 prompts, 8 heads of 128, bf16, rotated 43.5 us, not
+// rotated 33, fp32 58 (64 and 107 MB: 10 and 16 us of memory); bound by
+// instructions, of which a head's and a CTA's own are more than the values'.
+// One token of 8 sequences 3.7 us.
 //
 // U: units of 16 values that a thread holds of a page's head.  EACH: rotations
 // whose offset or halves no vector of eight respects.

@@ -210,9 +210,11 @@ struct QRows {
 //
 // Measured, heads 40 / 8 of 128, bf16: one sequence of 131071 tokens 62 us
 // (its rounds run at 7.0 TB/s; 3 us lie before the first copy, 10 behind the
-// last), 8 sequences to 8192 tokens 28 us, one token 7.6 us.  Registers are
-// kept free of spills: with the rings in shared memory little L1 is left, and
-// 50 spilled words a tile took a third of the time.
+// last), 8 sequences to 8192 tokens 29 us, one token 7.5 us.  With the rings in
+// shared memory little L1 is left for spilled registers: 50 words that every
+// tile stored and loaded took a third of the time.  bf16 kernels with 8 rows a
+// warp spill none; with 16 rows of 128 dimensions a warp 9 to 13 words are
+// spilled, elsewhere up to 3.
 template <int D, int NT, bool F32, int W>
 __global__ void __launch_bounds__(32 * W, W > 4 ? 1 : attend_wide_warps(D, NT) / 4)
     attend_kernel(const __grid_constant__ AttendParams p) {

@@ -304,11 +304,17 @@ AttendKernel attend_for(int head_dim, bool f32, const Launch& l) {
 
 // Wide up to one item (sequence, key head, row block) an SM: the parts of an
 // item to join are a third as many, and its phases have an SM's warps.  With
-// more items narrow CTAs run theirs side by side.  Heads 40 / 8 of 128, us
-// wide and narrow: 1 x 16000 tokens 20.0 and 29.2, 8 x 2000 18.9 and 22.9,
-// 8 x 4000 28.1 and 28.0, 64 x 200 28.8 and 22.1, 64 x 1000 54.6 and 39.3.
-// And where a sequence may be longer than a narrow CTA's round: at one token
-// 8.1 and 6.4.
+// more items narrow CTAs run theirs side by side.  5 query heads a key head, 8
+// key heads, bf16, us wide and narrow, sequences x tokens:
+//   heads of 128   1 x 8000 15.4 and 21.7, 1 x 16000 19.7 and 28.9, 8 x 1000 14.5
+//                  and 15.6, 8 x 8000 37.7 and 38.2, 16 x 1000 16.3 and 21.0; but
+//                  8 x 2000 21.2 and 19.1; beyond an item an SM 64 x 200 30.4
+//                  and 22.1, 64 x 1000 53.3 and 40.4
+//   heads of 256   1 x 8000 22.1 and 30.2, 8 x 8000 60.0 and 61.5
+//   heads of 64    1 x 8000 12.9 and 14.5, 16 x 1000 13.7 and 17.3; but 1 x 1000
+//                  12.0 and 10.3, 8 x 8000 30.7 and 27.8
+// And where a sequence may be longer than a narrow CTA's round (the lengths are
+// on the device, the table's width is what is known here): at one token 8.7 and 8.0.
 bool attend_wide(int64_t items, int sms, int64_t tokens, int narrow_round) {
   return items <= sms && tokens > narrow_round;
 }

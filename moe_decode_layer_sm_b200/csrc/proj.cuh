@@ -164,10 +164,10 @@ size_t proj_smem(int rows, int kb) {
 // fixed order, then the cluster's, pushed to the CTA that writes the output:
 // no scratch, no atomics.
 //
-// Measured: 131072 x 5120 MXFP4, 8 rows, 76 us (4.7 TB/s; the pair converter
-// and the scales keep the integer pipe busy, 158 instructions for 2048 codes);
-// 7168 x 5120 int4, 1 row 8.5 us, 8 rows 12 (the launch, x, 3.7 us of weights at
-// 5.1 TB/s on the 112 SMs that have an output block, the sums).
+// Measured: 131072 x 5120 MXFP4, 8 rows, 74.5 us (4.8 TB/s; 156 instructions for
+// 2048 codes; no pipe is full: issue 65 %, integer 55 %, tensor 27 %); 7168 x
+// 5120 int4, 1 row 8.1 us, 8 rows 10.5 (the launch, x, the weights on the 112 SMs
+// that have an output block, the sums: issue 62 % while a CTA runs); fp32 8 rows 14.3.
 template <bool F32, int SC, bool ZP>
 __global__ void __launch_bounds__(kProjThreads, 1) proj_kernel(const __grid_constant__ ProjParams p) {
   namespace cg = cooperative_groups;
