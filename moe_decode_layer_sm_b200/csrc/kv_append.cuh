@@ -188,9 +188,10 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
 // again, so codes and scales are those of the exact rotated values, rounded
 // once.  (A page's scale goes by all the tokens that a call writes to it, and
 // older codes are rounded again where it grows: a page filled token by token
-// may hold other codes than one written at once.)  Two sines and cosines a pair and page, shared by its heads, give all
-// the others by turning; a thread holds both halves of its pairs, so a value
-// costs one conversion each way and four binary64 operations.
+// may hold other codes than one written at once.)  Two sines and cosines a pair
+// and page, shared by its heads, give all the others by turning; a thread holds
+// both halves of its pairs, so a value costs one conversion each way and four
+// binary64 operations.
 //
 // Measured: 10486 tokens of 4 prompts, 8 heads of 128, bf16, rotated 43.5 us, not
 // rotated 33, fp32 58 (64 and 107 MB: 10 and 16 us of memory); bound by

@@ -160,9 +160,9 @@ size_t proj_smem(int rows, int kb) {
 // A group's scale multiplies the fp32 sum of its products.  (int4 codes as they
 // lie, fp16 subnormals, save that operation, but then the zero point has to come
 // off the sums, sum q x - z sum x, which loses weights near it: codes that equal
-// their zero point gave 1e-6 of sum z |x| s for 0.)  The warps' sums are added in a
-// fixed order, then the cluster's, pushed to the CTA that writes the output:
-// no scratch, no atomics.
+// their zero point gave 1e-6 of sum z |x| s for 0.)  The warps' sums are added
+// in a fixed order, then the cluster's, pushed to the CTA that writes the
+// output: no scratch, no atomics.
 //
 // Measured: 131072 x 5120 MXFP4, 8 rows, 74.5 us (4.8 TB/s; 156 instructions for
 // 2048 codes; no pipe is full: issue 65 %, integer 55 %, tensor 27 %); 7168 x
