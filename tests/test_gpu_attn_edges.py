@@ -8,7 +8,8 @@ import pytest
 import torch
 
 from tests import attn_reference as R
-from tests.test_gpu_attn import DT, check_append, gen, i32, make_cache, make_table, make_weights, normal, within
+from tests.test_gpu_attn import (DT, check_append, check_attend, gen, i32, make_cache, make_weights, normal,
+                                  within)
 
 pytestmark = pytest.mark.gpu
 
@@ -433,3 +434,17 @@ def test_attend_smallest_scales(m, dtype, d, hq, hk):
     if dtype == "bf16":
         more += 2.0 ** -134 + 448 * 2.0 ** -135
     within(out, want, ob + more)
+
+
+# ------------------------------------------------------- the largest calls
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_most_rows_and_most_sequences(m, dtype, d):
+    """128 query heads a key head with 8 new tokens each (1024 rows of one item),
+    and 4096 sequences, padding among them, in one call."""
+    check_attend(m, dtype, [300, 9, 65], [8, 8, 3], 8, 128, 1, d, 16)
+    lens = [1 + (7 * i) % 40 for i in range(4096)]
+    new = [0 if i % 9 == 4 else 1 + i % 2 for i in range(4096)]
+    check_attend(m, dtype, lens, new, 2, 2, 1, d, 16, window=30)
+    check_append(m, dtype, lens, [min(n, ln) for n, ln in zip(new, lens)], 2, 1, d, 16, m.Rope(d))
